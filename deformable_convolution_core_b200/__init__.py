@@ -31,6 +31,10 @@ DCN_F32, DCN_BF16, DCN_F16 = 0, 1, 2
 DTYPES = {"f32": DCN_F32, "float32": DCN_F32, "bf16": DCN_BF16, "bfloat16": DCN_BF16,
           "f16": DCN_F16, "float16": DCN_F16}
 
+# dcn_norm of include/dcn_core.h and the names accepted for it.
+DCN_NORM_NONE, DCN_NORM_LAYER, DCN_NORM_RMS = 0, 1, 2
+NORMS = {"none": DCN_NORM_NONE, "layer": DCN_NORM_LAYER, "rms": DCN_NORM_RMS}
+
 # Every entry point of include/dcn_core.h.
 EXPORTED_SYMBOLS = (
     "dcn_core_output_hw",
@@ -46,6 +50,15 @@ EXPORTED_SYMBOLS = (
     "dcn_core_offset_mask_projection",
     "dcn_core_linear_bf16",
     "dcn_core_offset_mask_guide_projection",
+    "dcn_core_fp8_pitch",
+    "dcn_core_quantize_fp8",
+    "dcn_core_linear_fp8_workspace",
+    "dcn_core_linear_fp8",
+    "dcn_core_linear_fp8_backward_workspace",
+    "dcn_core_linear_fp8_backward",
+    "dcn_core_block_norm",
+    "dcn_core_block_norm_backward_workspace",
+    "dcn_core_block_norm_backward",
     "dcn_core_sync_status",
     "dcn_status_string",
     "dcn_core_abi_version",
@@ -94,6 +107,36 @@ def problem_for(wl) -> DcnProblem:
     return make_problem(wl.N, wl.H, wl.W, wl.G, wl.Cg, wl.K, wl.stride, wl.pad, wl.dilation,
                         wl.offset_scale, wl.softmax, wl.dtype,
                         getattr(wl, "remove_center", 0))
+
+
+class DcnBlockNorm(ctypes.Structure):
+    """Mirror of ``dcn_block_norm`` in include/dcn_core.h."""
+    _fields_ = [("M", ctypes.c_int), ("C", ctypes.c_int), ("rows_per_gate", ctypes.c_int),
+                ("stream_dtype", ctypes.c_int), ("branch_dtype", ctypes.c_int),
+                ("post_norm", ctypes.c_int), ("pre_norm", ctypes.c_int),
+                ("post_eps", ctypes.c_float), ("pre_eps", ctypes.c_float),
+                ("residual_scale", ctypes.c_float)]
+
+    def __repr__(self):
+        return "DcnBlockNorm(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
+
+
+def make_block_norm(M, C, stream_dtype="bf16", branch_dtype=None, post_norm="none",
+                    pre_norm="layer", rows_per_gate=0, post_eps=1e-6, pre_eps=1e-6,
+                    residual_scale=1.0) -> DcnBlockNorm:
+    """branch_dtype defaults to the stream's type; rows_per_gate = 0 is one gate
+    vector for all rows."""
+    if isinstance(stream_dtype, str):
+        stream_dtype = DTYPES[stream_dtype]
+    if branch_dtype is None:
+        branch_dtype = stream_dtype
+    elif isinstance(branch_dtype, str):
+        branch_dtype = DTYPES[branch_dtype]
+    post_norm = NORMS[post_norm] if isinstance(post_norm, str) else post_norm
+    pre_norm = NORMS[pre_norm] if isinstance(pre_norm, str) else pre_norm
+    return DcnBlockNorm(int(M), int(C), int(rows_per_gate), int(stream_dtype), int(branch_dtype),
+                        int(post_norm), int(pre_norm), float(post_eps), float(pre_eps),
+                        float(residual_scale))
 
 
 def taps(problem: DcnProblem) -> int:
@@ -148,6 +191,25 @@ def load_library():
     lib.dcn_core_linear_bf16.argtypes = [vp, ctypes.c_int, ctypes.c_int, vp, ctypes.c_int, vp, vp,
                                          ctypes.c_int, vp]
     lib.dcn_core_linear_bf16.restype = st
+    ci, sz, npp = ctypes.c_int, ctypes.c_size_t, ctypes.POINTER(DcnBlockNorm)
+    lib.dcn_core_fp8_pitch.argtypes = [ci]
+    lib.dcn_core_fp8_pitch.restype = sz
+    lib.dcn_core_quantize_fp8.argtypes = [vp, ci, ci, ci, ci, vp, vp, vp, vp, vp]
+    lib.dcn_core_quantize_fp8.restype = st
+    lib.dcn_core_linear_fp8_workspace.argtypes = [ci, ci, ci]
+    lib.dcn_core_linear_fp8_workspace.restype = sz
+    lib.dcn_core_linear_fp8.argtypes = [vp, vp, ci, ci, vp, vp, ci, vp, vp, ci, vp, sz, vp]
+    lib.dcn_core_linear_fp8.restype = st
+    lib.dcn_core_linear_fp8_backward_workspace.argtypes = [ci, ci, ci]
+    lib.dcn_core_linear_fp8_backward_workspace.restype = sz
+    lib.dcn_core_linear_fp8_backward.argtypes = [vp, ci, ci, ci, ci] + [vp] * 8 + [sz, vp]
+    lib.dcn_core_linear_fp8_backward.restype = st
+    lib.dcn_core_block_norm.argtypes = [npp] + [vp] * 13
+    lib.dcn_core_block_norm.restype = st
+    lib.dcn_core_block_norm_backward_workspace.argtypes = [npp]
+    lib.dcn_core_block_norm_backward_workspace.restype = sz
+    lib.dcn_core_block_norm_backward.argtypes = [npp] + [vp] * 18 + [sz, vp]
+    lib.dcn_core_block_norm_backward.restype = st
     lib.dcn_core_sync_status.argtypes = [vp]
     lib.dcn_core_sync_status.restype = st
     lib.dcn_status_string.argtypes = [st]
@@ -317,13 +379,190 @@ def dcn_core_linear_bf16(input, M: int, K: int, weight, Nout: int, bias, output,
         int(out_dtype), _stream(stream)), "dcn_core_linear_bf16")
 
 
+def _torch_dtype(dtype: int) -> str:
+    return {DCN_F32: "torch.float32", DCN_BF16: "torch.bfloat16", DCN_F16: "torch.float16"}.get(
+        dtype, "")
+
+
+_CODES = ("torch.float8_e4m3fn", "torch.uint8")  # types a buffer of e4m3 codes may have
+
+
+def _arg(t, name: str, numel: int, dtypes) -> int | None:
+    """The address of one argument of the block operators.  A torch tensor must be
+    contiguous, on the current device, of one of `dtypes` and of exactly `numel`
+    elements (a program that passes another size has mixed two tensors up); None
+    and raw addresses go through as they are."""
+    if t is None or isinstance(t, int):
+        return t
+    if not hasattr(t, "data_ptr"):
+        raise TypeError(f"{name}: cannot pass {type(t)} as a pointer")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: tensors passed to the C ABI must be contiguous")
+    import torch
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name}: the tensor is on {t.device}, not on the current CUDA device")
+    if str(t.dtype) not in dtypes:
+        raise ValueError(f"{name}: expected {' or '.join(dtypes)}, got {t.dtype}")
+    if t.numel() != numel:
+        raise ValueError(f"{name}: expected {numel} elements, got {t.numel()}")
+    return t.data_ptr()
+
+
+def _workspace_arg(t, nbytes: int) -> int | None:
+    if t is not None and hasattr(t, "data_ptr"):
+        if t.numel() * t.element_size() < nbytes:
+            raise ValueError(f"workspace: {nbytes} bytes named, the tensor has "
+                             f"{t.numel() * t.element_size()}")
+        return _arg(t, "workspace", t.numel(), (str(t.dtype),))
+    return t
+
+
+_F32 = ("torch.float32",)
+
+
+def _ceil(a: int, b: int) -> int:
+    return -(-int(a) // b)
+
+
+def dcn_core_fp8_pitch(cols: int) -> int:
+    """Row pitch in bytes of an e4m3 matrix: 16 * ceil(cols / 16)."""
+    return int(load_library().dcn_core_fp8_pitch(int(cols)))
+
+
+def dcn_core_quantize_fp8(input, rows: int, cols: int, dtype, block_rows: int, q, scales, q_t=None,
+                          scales_t=None, stream=None) -> None:
+    """Block-scaled e4m3 of a (rows, cols) matrix, and of its transpose from the
+    same read (see include/dcn_core.h).  q (rows, pitch(cols)) with scales
+    (ceil(cols/128), rows) or, with block_rows = 128, (ceil(cols/128),
+    ceil(rows/128)); q_t (cols, pitch(rows)) with scales_t likewise; either pair
+    may be None."""
+    if isinstance(dtype, str):
+        dtype = DTYPES[dtype]
+    rows, cols = int(rows), int(cols)
+    kb, mb = _ceil(cols, 128), _ceil(rows, 128)
+    whole = block_rows == 128
+    _check(load_library().dcn_core_quantize_fp8(
+        _arg(input, "input", rows * cols, (_torch_dtype(dtype),)), int(dtype), rows, cols,
+        int(block_rows), _arg(q, "q", rows * _ceil(cols, 16) * 16, _CODES),
+        _arg(scales, "scales", kb * (mb if whole else rows), _F32),
+        _arg(q_t, "q_t", cols * _ceil(rows, 16) * 16, _CODES),
+        _arg(scales_t, "scales_t", mb * (kb if whole else cols), _F32), _stream(stream)),
+        "dcn_core_quantize_fp8")
+
+
+def dcn_core_linear_fp8_workspace(M: int, K: int, Nout: int) -> int:
+    return int(load_library().dcn_core_linear_fp8_workspace(int(M), int(K), int(Nout)))
+
+
+def dcn_core_linear_fp8(input, input_scales, M: int, K: int, weight, weight_scales, Nout: int, bias,
+                        output, out_dtype="bf16", workspace=None, workspace_bytes=0,
+                        stream=None) -> None:
+    """output (M, Nout) = input (M, K) @ weight (Nout, K).T + bias on block-scaled
+    e4m3 operands (see include/dcn_core.h): the input in blocks of 1 x 128, the
+    weight in blocks of 128 x 128, output in out_dtype."""
+    if isinstance(out_dtype, str):
+        out_dtype = DTYPES[out_dtype]
+    M, K, Nout = int(M), int(K), int(Nout)
+    kb, pitch = _ceil(K, 128), _ceil(K, 16) * 16
+    _check(load_library().dcn_core_linear_fp8(
+        _arg(input, "input", M * pitch, _CODES),
+        _arg(input_scales, "input_scales", kb * M, _F32), M, K,
+        _arg(weight, "weight", Nout * pitch, _CODES),
+        _arg(weight_scales, "weight_scales", kb * _ceil(Nout, 128), _F32), Nout,
+        _arg(bias, "bias", Nout, _F32),
+        _arg(output, "output", M * Nout, (_torch_dtype(out_dtype),)), int(out_dtype),
+        _workspace_arg(workspace, workspace_bytes), int(workspace_bytes), _stream(stream)),
+        "dcn_core_linear_fp8")
+
+
+def dcn_core_linear_fp8_backward_workspace(M: int, K: int, Nout: int) -> int:
+    return int(load_library().dcn_core_linear_fp8_backward_workspace(int(M), int(K), int(Nout)))
+
+
+def dcn_core_linear_fp8_backward(grad_out, dtype, M: int, K: int, Nout: int, weight_t,
+                                 weight_t_scales, input_t, input_t_scales, grad_input,
+                                 grad_weight, grad_bias, workspace, workspace_bytes,
+                                 stream=None) -> None:
+    """Gradients of dcn_core_linear_fp8 (see include/dcn_core.h).  weight_t and
+    input_t are the transposes dcn_core_quantize_fp8 writes (block_rows 128 and
+    1); grad_input has grad_out's type, grad_weight and grad_bias are fp32; a
+    gradient given as None is not computed."""
+    if isinstance(dtype, str):
+        dtype = DTYPES[dtype]
+    M, K, Nout = int(M), int(K), int(Nout)
+    td = (_torch_dtype(dtype),)
+    nb, mb = _ceil(Nout, 128), _ceil(M, 128)
+    _check(load_library().dcn_core_linear_fp8_backward(
+        _arg(grad_out, "grad_out", M * Nout, td), int(dtype), M, K, Nout,
+        _arg(weight_t, "weight_t", K * _ceil(Nout, 16) * 16, _CODES),
+        _arg(weight_t_scales, "weight_t_scales", nb * _ceil(K, 128), _F32),
+        _arg(input_t, "input_t", K * _ceil(M, 16) * 16, _CODES),
+        _arg(input_t_scales, "input_t_scales", mb * K, _F32),
+        _arg(grad_input, "grad_input", M * K, td),
+        _arg(grad_weight, "grad_weight", Nout * K, _F32),
+        _arg(grad_bias, "grad_bias", Nout, _F32), _workspace_arg(workspace, workspace_bytes),
+        int(workspace_bytes), _stream(stream)), "dcn_core_linear_fp8_backward")
+
+
+def dcn_core_block_norm(norm: DcnBlockNorm, residual, branch, gate, post_gamma, post_beta,
+                        pre_gamma, pre_beta, residual_out, normed, normed_scales=None,
+                        post_stats=None, pre_stats=None, stream=None) -> None:
+    """Post norm, gate, residual scale and the next pre norm in one pass (see
+    include/dcn_core.h).  With normed_scales given, normed takes e4m3 codes
+    (M, pitch(C)): the input of dcn_core_linear_fp8."""
+    M, C = norm.M, norm.C
+    sd, bd = (_torch_dtype(norm.stream_dtype),), (_torch_dtype(norm.branch_dtype),)
+    gates = _ceil(M, norm.rows_per_gate) if norm.rows_per_gate > 0 else 1
+    fp8 = normed_scales is not None
+    _check(load_library().dcn_core_block_norm(
+        ctypes.byref(norm), _arg(residual, "residual", M * C, sd), _arg(branch, "branch", M * C, bd),
+        _arg(gate, "gate", gates * C, _F32), _arg(post_gamma, "post_gamma", C, _F32),
+        _arg(post_beta, "post_beta", C, _F32), _arg(pre_gamma, "pre_gamma", C, _F32),
+        _arg(pre_beta, "pre_beta", C, _F32), _arg(residual_out, "residual_out", M * C, sd),
+        _arg(normed, "normed", M * (_ceil(C, 16) * 16 if fp8 else C), _CODES if fp8 else bd),
+        _arg(normed_scales, "normed_scales", _ceil(C, 128) * M, _F32),
+        _arg(post_stats, "post_stats", 2 * M, _F32), _arg(pre_stats, "pre_stats", 2 * M, _F32),
+        _stream(stream)), "dcn_core_block_norm")
+
+
+def dcn_core_block_norm_backward_workspace(norm: DcnBlockNorm) -> int:
+    return int(load_library().dcn_core_block_norm_backward_workspace(ctypes.byref(norm)))
+
+
+def dcn_core_block_norm_backward(norm: DcnBlockNorm, residual_out, branch, gate, post_gamma,
+                                 post_beta, pre_gamma, post_stats, pre_stats, grad_residual_out,
+                                 grad_normed, grad_residual, grad_branch, grad_gate=None,
+                                 grad_post_gamma=None, grad_post_beta=None, grad_pre_gamma=None,
+                                 grad_pre_beta=None, workspace=None, workspace_bytes=0,
+                                 stream=None) -> None:
+    """Gradients of dcn_core_block_norm (see include/dcn_core.h); a gradient given
+    as None is not computed."""
+    M, C = norm.M, norm.C
+    sd, bd = (_torch_dtype(norm.stream_dtype),), (_torch_dtype(norm.branch_dtype),)
+    gates = _ceil(M, norm.rows_per_gate) if norm.rows_per_gate > 0 else 1
+    vec = [_arg(t, n, C, _F32) for t, n in (
+        (grad_post_gamma, "grad_post_gamma"), (grad_post_beta, "grad_post_beta"),
+        (grad_pre_gamma, "grad_pre_gamma"), (grad_pre_beta, "grad_pre_beta"))]
+    _check(load_library().dcn_core_block_norm_backward(
+        ctypes.byref(norm), _arg(residual_out, "residual_out", M * C, sd),
+        _arg(branch, "branch", M * C, bd), _arg(gate, "gate", gates * C, _F32),
+        _arg(post_gamma, "post_gamma", C, _F32), _arg(post_beta, "post_beta", C, _F32),
+        _arg(pre_gamma, "pre_gamma", C, _F32), _arg(post_stats, "post_stats", 2 * M, _F32),
+        _arg(pre_stats, "pre_stats", 2 * M, _F32),
+        _arg(grad_residual_out, "grad_residual_out", M * C, sd),
+        _arg(grad_normed, "grad_normed", M * C, bd), _arg(grad_residual, "grad_residual", M * C, sd),
+        _arg(grad_branch, "grad_branch", M * C, bd), _arg(grad_gate, "grad_gate", gates * C, _F32),
+        *vec, _workspace_arg(workspace, workspace_bytes), int(workspace_bytes), _stream(stream)),
+        "dcn_core_block_norm_backward")
+
+
 def dcn_core_sync_status(stream=None) -> None:
     _check(load_library().dcn_core_sync_status(_stream(stream)), "dcn_core_sync_status")
 
 
-__all__ = ["DcnProblem", "DcnError", "make_problem", "problem_for", "taps", "load_library",
+__all__ = ["DcnProblem", "DcnBlockNorm", "DcnError", "make_problem", "make_block_norm", "problem_for", "taps", "load_library",
            "library_path", "EXPORTED_SYMBOLS", *EXPORTED_SYMBOLS, "ABI_VERSION",
            "DCN_CORE_NOALLOC_SCRATCH_BYTES",
            "DCN_OK", "DCN_ERR_INVALID_ARG", "DCN_ERR_UNSUPPORTED", "DCN_ERR_CUDA",
            "DCN_ERR_TIMEOUT", "DCN_ERR_OUT_OF_BOUNDS", "DCN_F32", "DCN_BF16", "DCN_F16",
-           "DTYPES"]
+           "DTYPES", "DCN_NORM_NONE", "DCN_NORM_LAYER", "DCN_NORM_RMS", "NORMS"]

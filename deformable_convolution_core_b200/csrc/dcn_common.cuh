@@ -12,14 +12,18 @@ namespace dcn {
 // bounded wait gave up, bit 1 = the bounds-checked build skipped an access
 // that would have left its tensor.
 constexpr unsigned int kErrTimeout = 1u, kErrOutOfBounds = 2u;
+#ifndef DCN_ERROR_WORD_BY_POINTER
 __device__ unsigned int g_dcn_error_word = 0;
+#endif
 
 // ---------------------------------------------------------------------------
 // Bounds-checked build (compiled with -DDCN_CHECK_BOUNDS), the substitute for
 // a memory checker: every global load, store and reduction of the kernels is
 // first tested against its tensor's extent, and an access that would leave it
 // is skipped and recorded in the error word.  Without the macro the tests
-// compile away.
+// compile away.  A translation unit that defines DCN_ERROR_WORD_BY_POINTER has
+// no word of its own: its kernels get the address of the library's one word
+// (DeviceInfo::error_word) and use in_range_of.
 // ---------------------------------------------------------------------------
 #ifdef DCN_CHECK_BOUNDS
 constexpr bool kCheckBounds = true;
@@ -27,6 +31,7 @@ constexpr bool kCheckBounds = true;
 constexpr bool kCheckBounds = false;
 #endif
 
+#ifndef DCN_ERROR_WORD_BY_POINTER
 // Element i of a tensor of n elements?
 __device__ __forceinline__ bool in_range(size_t i, size_t n) {
   if (!kCheckBounds) return true;
@@ -44,6 +49,16 @@ __device__ __forceinline__ bool in_tensor(const void* p, size_t nbytes, const vo
   if (!ok) atomicOr(&g_dcn_error_word, kErrOutOfBounds);
   return ok;
 }
+#else
+// Elements [i, i + k) of a tensor of n elements?
+__device__ __forceinline__ bool in_range_of(unsigned int* error_word, size_t i, size_t k,
+                                            size_t n) {
+  if (!kCheckBounds) return true;
+  const bool ok = i <= n && k <= n - i;
+  if (!ok) atomicOr(error_word, kErrOutOfBounds);
+  return ok;
+}
+#endif
 
 // ---------------------------------------------------------------------------
 // Division by a runtime-invariant divisor with one multiply-high and a shift

@@ -25,6 +25,7 @@
 #include "dcn_forward_tiled_wide.cuh"
 #include "dcn_guide.cuh"
 #include "dcn_guide_projection.cuh"
+#include "dcn_host.h"
 #include "dcn_projection.cuh"
 
 namespace dcn {
@@ -38,20 +39,6 @@ int64_t out_extent(int in, int K, int stride, int pad, int dil) {
   if (span < 0 || stride < 1) return 0;
   return span / stride + 1;
 }
-
-int esize(dcn_dtype d) { return d == DCN_F32 ? 4 : 2; }
-
-// Calls f with a value of the storage type of d (fp32, bf16 or fp16).
-template <typename F>
-auto with_storage(dcn_dtype d, F&& f) {
-  switch (d) {
-    case DCN_BF16: return f(__nv_bfloat16());
-    case DCN_F16: return f(__half());
-    default: return f(float());
-  }
-}
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // Width-axis stride, padding and dilation: the height ones unless separate_axes.
 int stride_w(const dcn_problem* p) { return p->separate_axes ? p->stride_w : p->stride; }
@@ -329,6 +316,8 @@ dcn_status check_forward_pointers(const dcn_problem* p, const void* x, const voi
 // Tiled forward (input box staged by TMA).
 // ---------------------------------------------------------------------------
 
+}  // namespace
+
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
     void* p = nullptr;
@@ -341,6 +330,8 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   }();
   return fn;
 }
+
+namespace {
 
 // Unique id of the current CUDA context (cuCtxGetId; 0 if it cannot be
 // read).  The per-device state the library keeps (the error word's address,
@@ -372,14 +363,8 @@ unsigned long long current_context_id() {
   return id;
 }
 
-struct DeviceInfo {
-  int sms = 0;
-  int smem_optin = 0;
-  unsigned int* error_word = nullptr;
-};
+}  // namespace
 
-// Per-device constants, looked up once per device (under a lock: calls may
-// come from several host threads).
 dcn_status device_info(DeviceInfo* out) {
   constexpr int kMaxDev = 64;
   static DeviceInfo cache[kMaxDev];
@@ -406,6 +391,8 @@ dcn_status device_info(DeviceInfo* out) {
   *out = cache[dev];
   return DCN_OK;
 }
+
+namespace {
 
 int env_int(const char* name, int dflt) {
   const char* s = std::getenv(name);

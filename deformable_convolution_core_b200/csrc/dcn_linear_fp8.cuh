@@ -1,0 +1,489 @@
+// Linear layer on block-scaled e4m3 operands (sm_100a tensor cores).
+//
+//   out[m, n] = sum_b sa[b, m] * sb[b, n] * (sum_{k in block b} A[m, k] * B[n, k]) + bias[n]
+//
+// The scales change every 128 products, and they are fp32 numbers, so a block's
+// products are summed on the tensor cores into a fresh accumulator in tensor
+// memory, and the blocks are added in fp32 registers with one packed FMA for two
+// values.  An e4m3 product has at most 8 significant bits, so a block's 128
+// products lose nothing but the rounding of their fp32 sum.
+//
+// Kernel: persistent CTAs over (128-row, BN-column, K split) items, columns
+// fastest (the row tile of A stays in L2 while B's column tiles pass).  Warp 0
+// streams 128-byte K blocks of A and B into a shared-memory ring by TMA (128-byte
+// swizzle); one thread of warp 1 issues tcgen05.mma (kind::f8f6f4, K = 32) for one
+// block at a time into one of 512 / BN accumulators; eight epilogue warps (four
+// lane quarters x two column halves) read each accumulator back, scale and add it,
+// and at an item's end store it by TMA through a swizzled 4 KB buffer each.  Every
+// mbarrier wait is bounded; on expiry the kernel sets the error word, stops issuing
+// work, waits (bounded) for what is in flight, frees its tensor memory and returns.
+#pragma once
+
+#include <cuda.h>
+
+#include "dcn_fp8.cuh"
+#include "dcn_ptx.cuh"
+
+namespace dcn {
+
+constexpr int kLfBM = 128;
+constexpr int kLfBK = 128;  // values and bytes of a K block: one scale, one swizzle atom
+constexpr int kLfEpiWarps = 8;
+constexpr int kLfThreads = (2 + kLfEpiWarps) * 32;
+constexpr uint32_t kLfTmemCols = 512;
+constexpr int kLfStoreBytes = 32 * 128;  // an epilogue warp's buffer: 32 rows of 128 bytes
+
+template <int BN>
+struct LfShape {
+  static constexpr int kStages = BN == 256 ? 4 : 6;
+  static constexpr int kAccs = int(kLfTmemCols) / BN;
+  static constexpr uint32_t kStageBytes = uint32_t(kLfBM + BN) * kLfBK;
+  static constexpr size_t kSmemBytes = 1024 /* alignment slack */ + size_t(kStages) * kStageBytes +
+                                       size_t(kLfEpiWarps) * kLfStoreBytes +
+                                       256 /* barriers, TMEM address */;
+};
+
+struct LinearArgs {
+  int M, N, K;
+  int k_blocks;            // ceil(K / 128)
+  int m_tiles, n_tiles;
+  int splits, kb_per;      // K splits and blocks of each (the last may have fewer)
+  int items;               // m_tiles * n_tiles * splits
+  int n_blocks;            // ceil(N / 128): pitch of sb with blocks of 128 rows
+  const float* sa;         // (k_blocks, M)
+  const float* sb;         // (k_blocks, n_blocks), or (k_blocks, N) with a scale a row
+  const float* bias;       // N values, or null
+  void* out;               // (splits, M, out_pitch) values of the output type
+  int out_pitch;
+  int tma_out;             // 1: rows are 16-byte multiples, stored by TMA
+  unsigned int* error_word;
+};
+
+// Instruction descriptor of kind::f8f6f4: e4m3 A and B (K-major), fp32 D, M x N.
+__device__ __forceinline__ uint32_t umma_idesc_e4m3_f32(int M, int N) {
+  return (1u << 4)                     // D format: fp32 (A and B format 0: e4m3)
+         | (uint32_t(N >> 3) << 17)    // N / 8
+         | (uint32_t(M >> 4) << 24);   // M / 16
+}
+
+__device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                          uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Store a (rows, 128-byte) box from shared memory; rows and columns outside the
+// tensor are left out.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int c0,
+                                             int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(smem_addr(src)), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+__device__ __forceinline__ void bulk_commit() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_wait_read0() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_wait0() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
+struct LinearItem {
+  int m0, n0, split, kb0, kb1;
+};
+
+template <int BN>
+__device__ __forceinline__ LinearItem linear_item(const LinearArgs& a, int item) {
+  LinearItem i;
+  const int nt = item % a.n_tiles, r = item / a.n_tiles;
+  i.split = r / a.m_tiles;
+  i.m0 = (r - i.split * a.m_tiles) * kLfBM;
+  i.n0 = nt * BN;
+  i.kb0 = i.split * a.kb_per;
+  i.kb1 = min(i.kb0 + a.kb_per, a.k_blocks);
+  return i;
+}
+
+// T: output type.  BN: column tile.  ROWB: sb holds a scale for each row of B (the
+// weight gradient), else one for each 128 rows.
+template <typename T, int BN, bool ROWB>
+__global__ void __launch_bounds__(kLfThreads, 1)
+    dcn_linear_fp8_kernel(const __grid_constant__ CUtensorMap amap,
+                          const __grid_constant__ CUtensorMap bmap,
+                          const __grid_constant__ CUtensorMap omap, const LinearArgs a) {
+  using S = LfShape<BN>;
+  constexpr int kHalf = BN / 2;  // columns of an epilogue warp
+  extern __shared__ __align__(1024) unsigned char lf_smem_raw[];
+  unsigned char* smem = lf_smem_raw + ((1024u - (smem_addr(lf_smem_raw) & 1023u)) & 1023u);
+  unsigned char* stage_a = smem;
+  unsigned char* stage_b = smem + size_t(S::kStages) * kLfBM * kLfBK;
+  unsigned char* store_buf = smem + size_t(S::kStages) * S::kStageBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(store_buf + kLfEpiWarps * kLfStoreBytes);
+  uint64_t* empty = full + S::kStages;
+  uint64_t* tfull = empty + S::kStages;   // accumulator ready
+  uint64_t* tempty = tfull + S::kAccs;    // accumulator read
+  uint64_t* mma_done = tempty + S::kAccs;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+  int* s_abort = reinterpret_cast<int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < S::kAccs; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], kLfEpiWarps);
+    }
+    mbar_init(mma_done, 1);
+    *s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(tmem_slot)),
+                 "r"(kLfTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  volatile int* abort_flag = s_abort;
+  auto give_up = [&]() {
+    atomicOr(a.error_word, kErrTimeout);
+    *abort_flag = 1;
+  };
+
+  if (warp == 0) {
+    // ---- TMA producer ----
+    if (lane == 0) {
+      uint32_t it = 0;
+      bool stop = false;
+      for (int item = blockIdx.x; item < a.items && !stop; item += gridDim.x) {
+        const LinearItem w = linear_item<BN>(a, item);
+        for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
+          if (*abort_flag) { stop = true; break; }
+          const int s = int(it % S::kStages);
+          const uint32_t u = it / S::kStages;
+          if (u > 0 && !mbar_wait_bounded(&empty[s], (u - 1) & 1)) {
+            give_up();
+            stop = true;
+            break;
+          }
+          mbar_arrive_expect_tx(&full[s], S::kStageBytes);
+          tma_load_2d(stage_a + size_t(s) * kLfBM * kLfBK, &amap, &full[s], kb * kLfBK, w.m0);
+          tma_load_2d(stage_b + size_t(s) * BN * kLfBK, &bmap, &full[s], kb * kLfBK, w.n0);
+        }
+      }
+      // the copies of the last issued stages may still be landing
+      for (uint32_t j = it > uint32_t(S::kStages) ? it - S::kStages : 0; j < it; ++j)
+        (void)mbar_wait_bounded(&full[j % S::kStages], (j / S::kStages) & 1);
+    }
+  } else if (warp == 1) {
+    // ---- MMA issuer: one K block, one accumulator ----
+    if (lane == 0) {
+      uint32_t it = 0;
+      bool stop = false;
+      for (int item = blockIdx.x; item < a.items && !stop; item += gridDim.x) {
+        const LinearItem w = linear_item<BN>(a, item);
+        const uint32_t idesc = umma_idesc_e4m3_f32(kLfBM, min(BN, (a.N - w.n0 + 15) / 16 * 16));
+        for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
+          const int acc = int(it % S::kAccs), s = int(it % S::kStages);
+          const uint32_t ua = it / S::kAccs;
+          if (*abort_flag || (ua > 0 && !mbar_wait_bounded(&tempty[acc], (ua - 1) & 1)) ||
+              !mbar_wait_bounded(&full[s], (it / S::kStages) & 1)) {
+            give_up();
+            stop = true;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t d = tmem_base + uint32_t(acc * BN);
+          const uint32_t a_addr = smem_addr(stage_a + size_t(s) * kLfBM * kLfBK);
+          const uint32_t b_addr = smem_addr(stage_b + size_t(s) * BN * kLfBK);
+          const int steps = min(4, (a.K - kb * kLfBK + 31) / 32);  // bytes behind K are zeros
+          for (int k = 0; k < steps; ++k)
+            umma_e4m3(d, umma_desc_sw128(a_addr + 32 * k), umma_desc_sw128(b_addr + 32 * k), idesc,
+                      uint32_t(k != 0));
+          umma_commit(&empty[s]);
+          umma_commit(&tfull[acc]);
+        }
+      }
+      // every MMA issued has retired before the accumulators are freed
+      umma_commit(mma_done);
+      (void)mbar_wait_bounded(mma_done, 0);
+    }
+  } else {
+    // ---- epilogue warps: TMEM lanes 32 (warp % 4) .. + 31, column half h ----
+    constexpr int kCols = 128 / int(sizeof(T));  // columns of a 128-byte store row
+    const int q = warp & 3, h = (warp - 2) >> 2;
+    unsigned char* buf = store_buf + (warp - 2) * kLfStoreBytes;
+    float* col_scale = reinterpret_cast<float*>(buf);  // ROWB: this block's column scales
+    uint32_t it = 0;
+    bool stop = false;
+    for (int item = blockIdx.x; item < a.items && !stop; item += gridDim.x) {
+      const LinearItem w = linear_item<BN>(a, item);
+      const int row = w.m0 + q * 32 + lane;
+      const int col0 = w.n0 + h * kHalf;
+      const int cols = min(kHalf, a.N - col0);  // columns of this warp inside the tensor
+      const float* sa = a.sa + row;
+      float2 acc[kHalf / 2];
+#pragma unroll
+      for (int i = 0; i < kHalf / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+      float s_next = row < a.M ? __ldg(sa + size_t(w.kb0) * a.M) : 0.f;
+      float w_next = 0.f, c_next[kHalf / 32];
+      auto load_b_scales = [&](int kb) {
+        if constexpr (ROWB) {
+#pragma unroll
+          for (int i = 0; i < kHalf / 32; ++i) {
+            const int c = i * 32 + lane;
+            c_next[i] = c < cols ? __ldg(a.sb + size_t(kb) * a.N + col0 + c) : 0.f;
+          }
+        } else {
+          w_next = cols > 0 ? __ldg(a.sb + size_t(kb) * a.n_blocks + col0 / kFp8Block) : 0.f;
+        }
+      };
+      load_b_scales(w.kb0);
+      if (ROWB) {  // the buffer's last store has been read
+        if (lane == 0) bulk_wait_read0();
+        __syncwarp();
+      }
+      for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
+        const int t = int(it % S::kAccs);
+        const float s_row = ROWB ? s_next : s_next * w_next;
+        if (ROWB) {
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < kHalf / 32; ++i) col_scale[i * 32 + lane] = c_next[i];
+          __syncwarp();
+        }
+        if (kb + 1 < w.kb1) {
+          s_next = row < a.M ? __ldg(sa + size_t(kb + 1) * a.M) : 0.f;
+          load_b_scales(kb + 1);
+        }
+        if (*abort_flag || !mbar_wait_bounded(&tfull[t], (it / S::kAccs) & 1)) {
+          give_up();
+          stop = true;
+          break;
+        }
+        tc_fence_after();
+        const float2 s2 = make_float2(s_row, s_row);
+#pragma unroll
+        for (int c = 0; c < kHalf / 32; ++c) {
+          if (c * 32 >= cols) break;
+          float v[32];
+          tmem_ld32(tmem_base + (uint32_t(q * 32) << 16) + uint32_t(t * BN + h * kHalf + c * 32),
+                    v);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float2 sc = s2;
+            if constexpr (ROWB) {
+              const float2 cs = *reinterpret_cast<const float2*>(col_scale + c * 32 + 2 * i);
+              sc = __fmul2_rn(s2, cs);
+            }
+            acc[c * 16 + i] = __ffma2_rn(make_float2(v[2 * i], v[2 * i + 1]), sc, acc[c * 16 + i]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tempty[t]);
+      }
+      if (stop) break;
+      // ---- the item's output: 32 rows x 128 bytes at a time ----
+#pragma unroll
+      for (int c = 0; c < kHalf / kCols; ++c) {
+        if (c * kCols >= cols) break;
+        if (lane == 0) bulk_wait_read0();
+        __syncwarp();
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {  // 16 bytes each
+          constexpr int kPer = 16 / int(sizeof(T));
+          float f[kPer];
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) {
+            const int j = c * kCols + g * kPer + i;
+            f[i] = (j & 1) ? acc[j >> 1].y : acc[j >> 1].x;
+            if (a.bias != nullptr) f[i] += j < cols ? __ldg(a.bias + col0 + j) : 0.f;
+          }
+          uint32_t p[4];
+          Storage<T>::pack(p, f);
+          *reinterpret_cast<uint4*>(buf + lane * 128 + ((g ^ (lane & 7)) << 4)) =
+              make_uint4(p[0], p[1], p[2], p[3]);
+        }
+        if (a.tma_out) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && w.m0 + q * 32 < a.M) {
+            tma_store_3d(&omap, buf, col0 + c * kCols, w.m0 + q * 32, w.split);
+            bulk_commit();
+          }
+        } else {
+          __syncwarp();
+          const int rows = min(32, a.M - (w.m0 + q * 32));
+          for (int r = 0; r < rows; ++r) {
+            const size_t o = (size_t(w.split) * a.M + size_t(w.m0 + q * 32 + r)) * a.out_pitch;
+#pragma unroll
+            for (int e = 0; e < kCols / 32; ++e) {
+              const int j = e * 32 + lane;  // column of the 128-byte row
+              const int byte = j * int(sizeof(T));
+              const T v = *reinterpret_cast<const T*>(buf + r * 128 +
+                                                      (((byte >> 4) ^ (r & 7)) << 4) + (byte & 15));
+              if (c * kCols + j < cols &&
+                  in_range_of(a.error_word, o + col0 + c * kCols + j, 1,
+                              size_t(a.splits) * a.M * a.out_pitch))
+                static_cast<T*>(a.out)[o + col0 + c * kCols + j] = v;
+            }
+          }
+          __syncwarp();
+        }
+      }
+    }
+    if (lane == 0) bulk_wait0();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
+                 "r"(kLfTmemCols)
+                 : "memory");
+  }
+}
+
+// out[m, n] = sum over the splits of part[s][m][n], in order, + bias[n].
+template <typename T>
+__global__ void __launch_bounds__(256)
+    dcn_linear_join_kernel(const float* part, int splits, int M, int N, int pitch,
+                           const float* bias, T* out) {
+  const size_t plane = size_t(M) * pitch, n = size_t(M) * N;
+  for (size_t i = size_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += size_t(gridDim.x) * 256) {
+    const size_t m = i / unsigned(N);
+    const int c = int(i - m * unsigned(N));
+    const float* p = part + m * pitch + c;
+    float v = p[0];
+    for (int s = 1; s < splits; ++s) v += p[s * plane];
+    if (bias) v += __ldg(bias + c);
+    Storage<T>::store_float(out + i, v);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Few rows.  The weight is read once and nothing else matters, so the work is
+// spread over many small CTAs instead of 128-row tiles: a CTA owns 8 output
+// columns, its 8 warps take the K blocks in turn, and mma.sync m16n8k32 multiplies
+// 16 rows by the 8 columns (rows that are not there cost no memory traffic).  A
+// lane reads 32 contiguous bytes of its weight row a block, two 16-byte loads; the
+// order of the 128 products is permuted the same way in both operands, so no
+// shuffle is needed.  The warps' sums are joined in shared memory in a fixed order.
+// ---------------------------------------------------------------------------
+struct LinearRowsArgs {
+  int M, N, K, k_blocks, pitch, n_blocks;
+  const uint8_t* a;
+  const uint8_t* b;
+  const float* sa;
+  const float* sb;
+  const float* bias;
+  void* out;
+  unsigned int* error_word;
+};
+
+constexpr int kLrWarps = 8;
+constexpr int kLrThreads = kLrWarps * 32;
+
+__device__ __forceinline__ void mma_e4m3_16x8x32(float (&d)[4], uint32_t a0, uint32_t a1,
+                                                 uint32_t a2, uint32_t a3, uint32_t b0,
+                                                 uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 32 bytes of a row of codes at byte k; bytes at or behind K are zeros.
+__device__ __forceinline__ void load_codes(const uint8_t* row, bool in, int k, int K, int pitch,
+                                           uint32_t (&w)[8]) {
+#pragma unroll
+  for (int v = 0; v < 2; ++v) {
+    uint4 x = make_uint4(0, 0, 0, 0);
+    const int k0 = k + 16 * v;
+    if (in && k0 < pitch) x = ldg128(row + k0);
+    w[4 * v] = x.x; w[4 * v + 1] = x.y; w[4 * v + 2] = x.z; w[4 * v + 3] = x.w;
+    if (k0 + 16 > K) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int left = K - (k0 + 4 * i);  // bytes of this word inside the row
+        if (left < 4) w[4 * v + i] &= left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+      }
+    }
+  }
+}
+
+template <typename T, int MT>  // MT: groups of 16 rows
+__global__ void __launch_bounds__(kLrThreads)
+    dcn_linear_fp8_rows_kernel(const LinearRowsArgs a) {
+  __shared__ float red[kLrWarps][MT * 16][8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int n0 = int(blockIdx.x) * 8;
+  const int m_base = int(blockIdx.y) * MT * 16;
+  const uint8_t* brow = a.b + size_t(min(n0 + g, a.N - 1)) * a.pitch;
+  float acc[MT][4];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[i][k] = 0.f;
+#pragma unroll 2
+  for (int kb = warp; kb < a.k_blocks; kb += kLrWarps) {
+    uint32_t wb[8];
+    load_codes(brow, n0 + g < a.N, kb * kFp8Block + 32 * t, a.K, a.pitch, wb);
+    const float sb = __ldg(a.sb + size_t(kb) * a.n_blocks + n0 / kFp8Block);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      uint32_t lo[8], hi[8];
+      const int m0 = m_base + i * 16 + g, m1 = m0 + 8;
+      load_codes(a.a + size_t(m0) * a.pitch, m0 < a.M, kb * kFp8Block + 32 * t, a.K, a.pitch, lo);
+      load_codes(a.a + size_t(m1) * a.pitch, m1 < a.M, kb * kFp8Block + 32 * t, a.K, a.pitch, hi);
+      const float s0 = m0 < a.M ? sb * __ldg(a.sa + size_t(kb) * a.M + m0) : 0.f;
+      const float s1 = m1 < a.M ? sb * __ldg(a.sa + size_t(kb) * a.M + m1) : 0.f;
+      float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        mma_e4m3_16x8x32(d, lo[2 * k], hi[2 * k], lo[2 * k + 1], hi[2 * k + 1], wb[2 * k],
+                         wb[2 * k + 1]);
+      acc[i][0] = fmaf(d[0], s0, acc[i][0]);
+      acc[i][1] = fmaf(d[1], s0, acc[i][1]);
+      acc[i][2] = fmaf(d[2], s1, acc[i][2]);
+      acc[i][3] = fmaf(d[3], s1, acc[i][3]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    *reinterpret_cast<float2*>(&red[warp][i * 16 + g][2 * t]) = make_float2(acc[i][0], acc[i][1]);
+    *reinterpret_cast<float2*>(&red[warp][i * 16 + g + 8][2 * t]) =
+        make_float2(acc[i][2], acc[i][3]);
+  }
+  __syncthreads();
+  for (int e = int(threadIdx.x); e < MT * 128; e += kLrThreads) {
+    const int m = m_base + (e >> 3), n = n0 + (e & 7);
+    if (m >= a.M || n >= a.N) continue;
+    float v = red[0][e >> 3][e & 7];
+#pragma unroll
+    for (int w = 1; w < kLrWarps; ++w) v += red[w][e >> 3][e & 7];
+    if (a.bias) v += __ldg(a.bias + n);
+    const size_t o = size_t(m) * a.N + n;
+    if (in_range_of(a.error_word, o, 1, size_t(a.M) * a.N))
+      Storage<T>::store_float(static_cast<T*>(a.out) + o, v);
+  }
+}
+
+}  // namespace dcn

@@ -1,6 +1,5 @@
 // Shared pieces of the kernels that stage the input in shared memory by TMA
-// (sm_100a): the work-item decomposition, the box geometry, and the mbarrier
-// and bulk-tensor-copy primitives.
+// (sm_100a): the work-item decomposition and the box geometry.
 //
 // A persistent CTA walks work items (image n, output tile, group g).  For
 // each item one TMA tensor copy brings the group's Cg channels of the input
@@ -13,6 +12,7 @@
 #include <cuda.h>
 
 #include "dcn_common.cuh"
+#include "dcn_ptx.cuh"
 #include "dcn_tile.cuh"
 
 namespace dcn {
@@ -39,82 +39,6 @@ struct TiledParams {
   FastDiv fd_G, fd_nTX, fd_tiles, fd_TW;
 };
 
-__device__ __forceinline__ uint32_t smem_addr(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-
-__device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(count)
-               : "memory");
-}
-
-__device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t* bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)),
-               "r"(bytes)
-               : "memory");
-}
-
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
-}
-
-__device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-      " selp.u32 %0, 1, 0, p;\n}"
-      : "=r"(done)
-      : "r"(smem_addr(bar)), "r"(parity)
-      : "memory");
-  return done != 0;
-}
-
-// try_wait with a suspend-time hint: the thread may sleep up to `ns`
-// nanoseconds inside the instruction instead of spinning on issue slots; it
-// returns as soon as the phase completes.
-__device__ __forceinline__ bool mbar_try_wait_sleep(uint64_t* bar, uint32_t parity, uint32_t ns) {
-  uint32_t done;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
-      " selp.u32 %0, 1, 0, p;\n}"
-      : "=r"(done)
-      : "r"(smem_addr(bar)), "r"(parity), "r"(ns)
-      : "memory");
-  return done != 0;
-}
-
-__device__ __forceinline__ uint64_t global_ns() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-  return t;
-}
-
-// Bounded wait for the phase with the given parity: gives up after 2^22
-// polls or one second, whichever comes first.
-__device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = global_ns();
-  for (uint32_t i = 0; i < (1u << 22); ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 255u) == 255u && global_ns() - t0 > 1000000000ull) return false;
-  }
-  return false;
-}
-
-// The same bound (one second) for waits that may be long (a consumer waiting
-// for its box, a producer waiting for a free buffer): each poll sleeps up to 2
-// microseconds inside try_wait, so waiting warps leave the issue slots to the
-// working ones.
-__device__ __forceinline__ bool mbar_wait_bounded_sleep(uint64_t* bar, uint32_t parity) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = global_ns();
-  for (uint32_t i = 0; i < (1u << 20); ++i) {
-    if (mbar_try_wait_sleep(bar, parity, 2000u)) return true;
-    if ((i & 15u) == 15u && global_ns() - t0 > 1000000000ull) return false;
-  }
-  return false;
-}
-
 __device__ __forceinline__ void tma_load_box(void* dst, const CUtensorMap* map, uint64_t* bar,
                                              int c0, int c1, int c2, int c3) {
   asm volatile(
@@ -123,46 +47,6 @@ __device__ __forceinline__ void tma_load_box(void* dst, const CUtensorMap* map, 
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3),
       "r"(smem_addr(bar))
       : "memory");
-}
-
-__device__ __forceinline__ void fence_proxy_async_smem() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
-__device__ __forceinline__ uint4 lds128(const void* p) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(smem_addr(p)));
-  return v;
-}
-
-// The same from a 32-bit shared-window address.
-__device__ __forceinline__ uint4 lds128_a(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a));
-  return v;
-}
-
-__device__ __forceinline__ uint4 ldg128(const void* p) {
-  uint4 v;
-  asm("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];"
-      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-      : "l"(p));
-  return v;
-}
-
-// 16 bytes from global memory, zeros unless pred (a false predicate issues no access).
-__device__ __forceinline__ uint4 ldg128_pred(const void* p, bool pred) {
-  uint4 v;
-  asm("{\n .reg .pred q;\n setp.ne.b32 q, %5, 0;\n"
-      " mov.b32 %0, 0;\n mov.b32 %1, 0;\n mov.b32 %2, 0;\n mov.b32 %3, 0;\n"
-      " @q ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];\n}"
-      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-      : "l"(p), "r"(int(pred)));
-  return v;
 }
 
 // Item -> (n, ho0, wo0, g); g is the fastest index, so consecutive items of a

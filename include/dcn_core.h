@@ -369,6 +369,188 @@ DCN_API dcn_status dcn_core_linear_bf16(const void* input, int M, int K, const v
                                         int Nout, const float* bias, void* output,
                                         dcn_dtype out_dtype, cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * The block around the core operator: x += gate * DCNv3(norm(x)), then
+ * x += gate * MLP(norm(x)) (InternImage-L DCNv3 explainer (wmrh.cn), section
+ * 四), with norms before or behind the branch, and its linear layers on 8-bit
+ * floating-point operands.
+ *
+ * e4m3 operands.  A matrix (rows, cols) is held as
+ *   codes   e4m3 (one byte a value), row-major with a row pitch of
+ *           dcn_core_fp8_pitch(cols) = 16 * ceil(cols / 16) bytes; the bytes
+ *           behind a row's last column are written as zeros and never used
+ *   scales  fp32, (ceil(cols / 128), R), R = rows with block_rows = 1 and
+ *           ceil(rows / 128) with block_rows = 128: scales[b * R + r] belongs to
+ *           columns 128 b .. 128 b + 127 of row r (of rows 128 r .. 128 r + 127)
+ * and stands for code * scale.  Over the values x of one block,
+ *   a = max(max |x|, 7 * 2^-58),  scale = a / 448,  inv = 448 / a,
+ *   code = e4m3(x * inv),
+ * every operation rounded to fp32 (the code to the nearest e4m3 value, ties to
+ * even).  448 is the largest e4m3 value; the floor keeps an all-zero block (scale
+ * 2^-64) and inv finite.  A block that holds a NaN or an infinity gets the scale
+ * NaN and NaN codes, so that whatever it takes part in becomes NaN.
+ * Sizes are 64-bit products: a matrix may hold 2^31 values and more.
+ * ------------------------------------------------------------------------- */
+
+/* Row pitch in bytes of an e4m3 matrix with `cols` columns (0 for cols < 1). */
+DCN_API size_t dcn_core_fp8_pitch(int cols);
+
+/*
+ * Quantise a matrix to e4m3 with a scale for each block, and its transpose from
+ * the same read.
+ *   input     device, (rows, cols) of dtype, dense; 16-byte aligned
+ *   block_rows  1: blocks of 1 x 128 (activations, gradients); 128: blocks of
+ *             128 x 128 (weights)
+ *   q, scales      the matrix (rows, cols), blocks along its columns; both NULL to leave out
+ *   q_t, scales_t  the transpose (cols, rows), blocks along the input's rows
+ *             (128 x 1 of the input, or the same 128 x 128 blocks); both NULL to leave out
+ * One of the two pairs at least.  q and q_t 16-byte, scales 4-byte aligned; no
+ * output overlaps the input or another output.
+ */
+DCN_API dcn_status dcn_core_quantize_fp8(const void* input, dcn_dtype dtype, int rows, int cols,
+                                         int block_rows, void* q, float* scales, void* q_t,
+                                         float* scales_t, cudaStream_t stream);
+
+/* Device workspace dcn_core_linear_fp8 needs, in bytes: room for the partial
+ * products when the inner length is split over the SMs (few output tiles), else
+ * 0 (also for invalid sizes).  Depends on the current device. */
+DCN_API size_t dcn_core_linear_fp8_workspace(int M, int K, int Nout);
+
+/*
+ * A linear layer of the block on e4m3 operands (the form of dcn_core_linear_bf16
+ * at twice its tensor-core rate and half its operand bytes):
+ *     output[m, j] = sum_b input_scales[b, m] * weight_scales[b, j / 128]
+ *                    * (sum_{c in block b} input[m, c] * weight[j, c]) + bias[j]
+ *   input   e4m3 (M, K), input_scales (ceil(K/128), M): block_rows = 1
+ *   weight  e4m3 (Nout, K), weight_scales (ceil(K/128), ceil(Nout/128)): block_rows = 128
+ *   bias    device, fp32, (Nout), or NULL
+ *   output  device, (M, Nout) in out_dtype, dense, written entirely
+ * The products of a block of 128 are summed in fp32 on the tensor cores, the
+ * blocks in fp32 registers; each output is rounded once.  The result is the same
+ * for every run (no atomics).  input, weight, output and workspace 16-byte
+ * aligned (else DCN_ERR_UNSUPPORTED); workspace may be NULL when its size is 0,
+ * a missing or short one is DCN_ERR_INVALID_ARG; its contents on entry are
+ * irrelevant, and calls that may overlap need one each.
+ */
+DCN_API dcn_status dcn_core_linear_fp8(const void* input, const float* input_scales, int M, int K,
+                                       const void* weight, const float* weight_scales, int Nout,
+                                       const float* bias, void* output, dcn_dtype out_dtype,
+                                       void* workspace, size_t workspace_bytes,
+                                       cudaStream_t stream);
+
+/* Device workspace dcn_core_linear_fp8_backward needs, in bytes (0 for invalid
+ * sizes): the quantised grad_out, its transpose, their scales, and partial sums. */
+DCN_API size_t dcn_core_linear_fp8_backward_workspace(int M, int K, int Nout);
+
+/*
+ * Backward of dcn_core_linear_fp8.  grad_out is quantised twice from one read,
+ * along its columns for grad_input and along its rows for grad_weight (the
+ * gradients pass through the quantisation of input and weight unchanged):
+ *     grad_input[m, c]  = sum_j Q(grad_out)[m, j] * weight[j, c]
+ *     grad_weight[j, c] = sum_m Q(grad_out^T)[j, m] * input[m, c]
+ *     grad_bias[j]      = sum_m grad_out[m, j]           (unquantised, fp32)
+ *   grad_out  device, (M, Nout) of dtype, dense
+ *   weight_t  e4m3 (K, Nout) with weight_t_scales (ceil(Nout/128), ceil(K/128)):
+ *             the transpose that dcn_core_quantize_fp8 writes with block_rows = 128
+ *   input_t   e4m3 (K, M) with input_t_scales (ceil(M/128), K): the transpose
+ *             that it writes with block_rows = 1
+ *   grad_input (M, K) of dtype; grad_weight fp32 (Nout, K); grad_bias fp32 (Nout);
+ *             each may be NULL and is then not computed (one at least is given;
+ *             weight_t may be NULL without grad_input, input_t without grad_weight)
+ * Matrices and workspace 16-byte aligned; errors as for dcn_core_linear_fp8.
+ */
+DCN_API dcn_status dcn_core_linear_fp8_backward(
+    const void* grad_out, dcn_dtype dtype, int M, int K, int Nout, const void* weight_t,
+    const float* weight_t_scales, const void* input_t, const float* input_t_scales,
+    void* grad_input, float* grad_weight, float* grad_bias, void* workspace,
+    size_t workspace_bytes, cudaStream_t stream);
+
+typedef enum {
+  DCN_NORM_NONE = 0,
+  DCN_NORM_LAYER = 1,  /* (v - mean) / sqrt(var + eps), biased variance over the channels */
+  DCN_NORM_RMS = 2     /* v / sqrt(mean(v^2) + eps)                                       */
+} dcn_norm;
+
+/*
+ * Description of a block norm: what stands between one branch of the block and
+ * the next.
+ *   M, C           rows (pixels of all images) and channels, >= 1; C <= 5120
+ *   rows_per_gate  0: one gate vector for all rows; n >= 1: rows n b .. n b + n - 1
+ *                  take gate vector b (one a sample: stochastic depth, modulation)
+ *   stream_dtype   storage type of the residual stream
+ *   branch_dtype   storage type of the branch output and of the normed output;
+ *                  the stream's type, or 2-byte with an fp32 stream
+ *   post_norm      norm of the branch output;  pre_norm  norm of the new stream
+ *   post_eps, pre_eps  finite, >= 0 (read with the norm)
+ *   residual_scale finite factor of the old stream
+ */
+typedef struct {
+  int M, C;
+  int rows_per_gate;
+  dcn_dtype stream_dtype, branch_dtype;
+  dcn_norm post_norm, pre_norm;
+  float post_eps, pre_eps;
+  float residual_scale;
+} dcn_block_norm;
+
+/*
+ * The norms behind one branch and before the next, with the branch's gate and
+ * the residual scale, in one pass:
+ *     p = post_norm(branch) * post_gamma + post_beta      (p = branch without a post norm)
+ *     r = residual_scale * residual + gate * p            -> residual_out
+ *     h = pre_norm(r) * pre_gamma + pre_beta              -> normed
+ * All arithmetic is fp32 on unrounded values (h is taken of r before r is
+ * rounded); each output is rounded once.
+ *   residual   (M, C) of stream_dtype;  branch  (M, C) of branch_dtype, or NULL: the
+ *              term is left out (the first norm of a stage; post_norm must be NONE)
+ *   gate       fp32 (ceil(M / rows_per_gate), C) or (1, C), or NULL (1)
+ *   *_gamma, *_beta  fp32 (C), each may be NULL (1 and 0)
+ *   residual_out  (M, C) of stream_dtype, or NULL; may be `residual` itself
+ *   normed     with pre_norm: (M, C) of branch_dtype, or, with normed_scales given,
+ *              e4m3 codes with row pitch dcn_core_fp8_pitch(C) quantised in blocks
+ *              of 1 x 128 from the unrounded h, scales (ceil(C/128), M): the input
+ *              of dcn_core_linear_fp8.  NULL without pre_norm
+ *   post_stats, pre_stats  fp32 (2, M): mean (0 for RMS) and 1/sqrt(...) of each
+ *              row, for the backward; each may be NULL
+ * residual_out or normed at least.  Matrices 16-byte aligned, vectors 16-byte,
+ * scales and statistics 4-byte.
+ */
+DCN_API dcn_status dcn_core_block_norm(const dcn_block_norm* norm, const void* residual,
+                                       const void* branch, const float* gate,
+                                       const float* post_gamma, const float* post_beta,
+                                       const float* pre_gamma, const float* pre_beta,
+                                       void* residual_out, void* normed, float* normed_scales,
+                                       float* post_stats, float* pre_stats, cudaStream_t stream);
+
+/* Device workspace dcn_core_block_norm_backward needs, in bytes: partial sums of
+ * the parameters' gradients (0 for an invalid description).  Depends on the
+ * current device. */
+DCN_API size_t dcn_core_block_norm_backward_workspace(const dcn_block_norm* norm);
+
+/*
+ * Backward of dcn_core_block_norm.
+ *   residual_out  the forward's r (M, C);  branch, gate, post_gamma, post_beta,
+ *              pre_gamma, post_stats, pre_stats: the forward's
+ *   grad_residual_out  gradient of r from the rest of the stream, (M, C) of
+ *              stream_dtype, or NULL (0)
+ *   grad_normed  gradient of h, (M, C) of branch_dtype; NULL without pre_norm
+ *   grad_residual  (M, C) of stream_dtype, or NULL; may be grad_residual_out itself
+ *   grad_branch    (M, C) of branch_dtype; NULL only without a branch
+ *   grad_gate      fp32, the gate's shape;  grad_post_gamma, grad_post_beta,
+ *              grad_pre_gamma, grad_pre_beta: fp32 (C); each may be NULL
+ * Sums over rows run in a fixed order (no atomics): the same inputs give the same
+ * bits on the same device.  workspace 16-byte aligned, contents on entry
+ * irrelevant; missing or short: DCN_ERR_INVALID_ARG.  A gate for each row
+ * (rows_per_gate = 1) is right but slow.
+ */
+DCN_API dcn_status dcn_core_block_norm_backward(
+    const dcn_block_norm* norm, const void* residual_out, const void* branch, const float* gate,
+    const float* post_gamma, const float* post_beta, const float* pre_gamma,
+    const float* post_stats, const float* pre_stats, const void* grad_residual_out,
+    const void* grad_normed, void* grad_residual, void* grad_branch, float* grad_gate,
+    float* grad_post_gamma, float* grad_post_beta, float* grad_pre_gamma, float* grad_pre_beta,
+    void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
 /* Synchronises `stream` and reports: DCN_ERR_CUDA if CUDA reports an error,
  * DCN_ERR_OUT_OF_BOUNDS if the bounds-checked build (compiled with
  * -DDCN_CHECK_BOUNDS) skipped an access outside a tensor, DCN_ERR_TIMEOUT if a
