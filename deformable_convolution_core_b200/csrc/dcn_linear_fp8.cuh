@@ -12,11 +12,16 @@
 // fastest (the row tile of A stays in L2 while B's column tiles pass).  Warp 0
 // streams 128-byte K blocks of A and B into a shared-memory ring by TMA (128-byte
 // swizzle); one thread of warp 1 issues tcgen05.mma (kind::f8f6f4, K = 32) for one
-// block at a time into one of 512 / BN accumulators; eight epilogue warps (four
-// lane quarters x two column halves) read each accumulator back, scale and add it,
-// and at an item's end store it by TMA through a swizzled 4 KB buffer each.  Every
-// mbarrier wait is bounded; on expiry the kernel sets the error word, stops issuing
-// work, waits (bounded) for what is in flight, frees its tensor memory and returns.
+// block at a time into one of 512 / BN accumulators; warp 2 brings the blocks'
+// scales into a ring of their own with asynchronous copies; sixteen epilogue warps
+// (four lane quarters x four column quarters) read each accumulator back, scale and
+// add it, and at an item's end store it through a swizzled 4 KB buffer each.  The
+// sums of a 128 x 256 tile take 64 of the 96 registers of every epilogue thread, and
+// four epilogue warps a scheduler hide each other's tensor-memory reads.  (Eight
+// warps with 128 sums a thread spill, with or without registers moved to them.)
+// Every mbarrier wait is bounded; on expiry the kernel sets the error word, stops
+// issuing work, waits (bounded) for what is in flight, frees its tensor memory and
+// returns.
 #pragma once
 
 #include <cuda.h>
@@ -28,18 +33,22 @@ namespace dcn {
 
 constexpr int kLfBM = 128;
 constexpr int kLfBK = 128;  // values and bytes of a K block: one scale, one swizzle atom
-constexpr int kLfEpiWarps = 8;
-constexpr int kLfThreads = (2 + kLfEpiWarps) * 32;
+constexpr int kLfFrontWarps = 4;  // TMA, MMA, scales, none
+constexpr int kLfEpiWarps = 16;
+constexpr int kLfThreads = (kLfFrontWarps + kLfEpiWarps) * 32;
 constexpr uint32_t kLfTmemCols = 512;
 constexpr int kLfStoreBytes = 32 * 128;  // an epilogue warp's buffer: 32 rows of 128 bytes
+constexpr int kLfScaleSlots = 4;         // K blocks whose scales are in flight
 
 template <int BN>
 struct LfShape {
-  static constexpr int kStages = BN == 256 ? 4 : 6;
+  static constexpr int kStages = BN == 256 ? 3 : 4;
   static constexpr int kAccs = int(kLfTmemCols) / BN;
   static constexpr uint32_t kStageBytes = uint32_t(kLfBM + BN) * kLfBK;
+  static constexpr int kScaleFloats = kLfBM + BN;  // a slot: row scales, column scales
   static constexpr size_t kSmemBytes = 1024 /* alignment slack */ + size_t(kStages) * kStageBytes +
                                        size_t(kLfEpiWarps) * kLfStoreBytes +
+                                       size_t(kLfScaleSlots) * kScaleFloats * 4 +
                                        256 /* barriers, TMEM address */;
 };
 
@@ -55,7 +64,7 @@ struct LinearArgs {
   const float* bias;       // N values, or null
   void* out;               // (splits, M, out_pitch) values of the output type
   int out_pitch;
-  int tma_out;             // 1: rows are 16-byte multiples, stored by TMA
+  int vec_out;             // 1: rows start on 16-byte boundaries: vector stores
   unsigned int* error_word;
 };
 
@@ -75,24 +84,39 @@ __device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint
       : "memory");
 }
 
-// Store a (rows, 128-byte) box from shared memory; rows and columns outside the
-// tensor are left out.
-__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int c0,
-                                             int c1, int c2) {
+// 16 consecutive fp32 columns of this warp's TMEM lanes, asynchronously: the values
+// are there after tmem_wait16 of the same registers.
+__device__ __forceinline__ void tmem_ld16_async(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
-          reinterpret_cast<uint64_t>(map)),
-      "r"(smem_addr(src)), "r"(c0), "r"(c1), "r"(c2)
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void bulk_commit() {
-  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+// Waits for the thread's TMEM loads; the registers pass through, so that no use of
+// them can move in front of the wait.
+__device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
 }
-__device__ __forceinline__ void bulk_wait_read0() {
-  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+
+// An asynchronous 4-byte copy to shared memory; zero where `in` is false.
+__device__ __forceinline__ void cp_async4(float* dst, const float* src, bool in) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_addr(dst)), "l"(src),
+               "r"(in ? 4 : 0)
+               : "memory");
 }
-__device__ __forceinline__ void bulk_wait0() {
-  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+// One arrival on `bar` when all copies of this thread so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar))
+               : "memory");
 }
 
 struct LinearItem {
@@ -116,20 +140,22 @@ __device__ __forceinline__ LinearItem linear_item(const LinearArgs& a, int item)
 template <typename T, int BN, bool ROWB>
 __global__ void __launch_bounds__(kLfThreads, 1)
     dcn_linear_fp8_kernel(const __grid_constant__ CUtensorMap amap,
-                          const __grid_constant__ CUtensorMap bmap,
-                          const __grid_constant__ CUtensorMap omap, const LinearArgs a) {
+                          const __grid_constant__ CUtensorMap bmap, const LinearArgs a) {
   using S = LfShape<BN>;
-  constexpr int kHalf = BN / 2;  // columns of an epilogue warp
+  constexpr int kWide = BN / 4;  // columns of an epilogue warp
   extern __shared__ __align__(1024) unsigned char lf_smem_raw[];
   unsigned char* smem = lf_smem_raw + ((1024u - (smem_addr(lf_smem_raw) & 1023u)) & 1023u);
   unsigned char* stage_a = smem;
   unsigned char* stage_b = smem + size_t(S::kStages) * kLfBM * kLfBK;
   unsigned char* store_buf = smem + size_t(S::kStages) * S::kStageBytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(store_buf + kLfEpiWarps * kLfStoreBytes);
+  float* scale_ring = reinterpret_cast<float*>(store_buf + kLfEpiWarps * kLfStoreBytes);
+  uint64_t* full = reinterpret_cast<uint64_t*>(scale_ring + kLfScaleSlots * S::kScaleFloats);
   uint64_t* empty = full + S::kStages;
   uint64_t* tfull = empty + S::kStages;   // accumulator ready
   uint64_t* tempty = tfull + S::kAccs;    // accumulator read
-  uint64_t* mma_done = tempty + S::kAccs;
+  uint64_t* sfull = tempty + S::kAccs;    // scales landed
+  uint64_t* sempty = sfull + kLfScaleSlots;
+  uint64_t* mma_done = sempty + kLfScaleSlots;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
   int* s_abort = reinterpret_cast<int*>(tmem_slot + 1);
 
@@ -138,6 +164,10 @@ __global__ void __launch_bounds__(kLfThreads, 1)
     for (int s = 0; s < S::kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < kLfScaleSlots; ++s) {
+      mbar_init(&sfull[s], 32);
+      mbar_init(&sempty[s], kLfEpiWarps);
     }
     for (int b = 0; b < S::kAccs; ++b) {
       mbar_init(&tfull[b], 1);
@@ -222,132 +252,151 @@ __global__ void __launch_bounds__(kLfThreads, 1)
       umma_commit(mma_done);
       (void)mbar_wait_bounded(mma_done, 0);
     }
-  } else {
-    // ---- epilogue warps: TMEM lanes 32 (warp % 4) .. + 31, column half h ----
-    constexpr int kCols = 128 / int(sizeof(T));  // columns of a 128-byte store row
-    const int q = warp & 3, h = (warp - 2) >> 2;
-    unsigned char* buf = store_buf + (warp - 2) * kLfStoreBytes;
-    float* col_scale = reinterpret_cast<float*>(buf);  // ROWB: this block's column scales
+  } else if (warp == 2) {
+    // ---- scales ----
     uint32_t it = 0;
     bool stop = false;
     for (int item = blockIdx.x; item < a.items && !stop; item += gridDim.x) {
       const LinearItem w = linear_item<BN>(a, item);
-      const int row = w.m0 + q * 32 + lane;
-      const int col0 = w.n0 + h * kHalf;
-      const int cols = min(kHalf, a.N - col0);  // columns of this warp inside the tensor
-      const float* sa = a.sa + row;
-      float2 acc[kHalf / 2];
-#pragma unroll
-      for (int i = 0; i < kHalf / 2; ++i) acc[i] = make_float2(0.f, 0.f);
-      float s_next = row < a.M ? __ldg(sa + size_t(w.kb0) * a.M) : 0.f;
-      float w_next = 0.f, c_next[kHalf / 32];
-      auto load_b_scales = [&](int kb) {
-        if constexpr (ROWB) {
-#pragma unroll
-          for (int i = 0; i < kHalf / 32; ++i) {
-            const int c = i * 32 + lane;
-            c_next[i] = c < cols ? __ldg(a.sb + size_t(kb) * a.N + col0 + c) : 0.f;
-          }
-        } else {
-          w_next = cols > 0 ? __ldg(a.sb + size_t(kb) * a.n_blocks + col0 / kFp8Block) : 0.f;
-        }
-      };
-      load_b_scales(w.kb0);
-      if (ROWB) {  // the buffer's last store has been read
-        if (lane == 0) bulk_wait_read0();
-        __syncwarp();
-      }
       for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
-        const int t = int(it % S::kAccs);
-        const float s_row = ROWB ? s_next : s_next * w_next;
-        if (ROWB) {
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < kHalf / 32; ++i) col_scale[i * 32 + lane] = c_next[i];
-          __syncwarp();
-        }
-        if (kb + 1 < w.kb1) {
-          s_next = row < a.M ? __ldg(sa + size_t(kb + 1) * a.M) : 0.f;
-          load_b_scales(kb + 1);
-        }
-        if (*abort_flag || !mbar_wait_bounded(&tfull[t], (it / S::kAccs) & 1)) {
+        const int s = int(it % kLfScaleSlots);
+        const uint32_t u = it / kLfScaleSlots;
+        if (*abort_flag || (u > 0 && !mbar_wait_bounded(&sempty[s], (u - 1) & 1))) {
           give_up();
           stop = true;
           break;
         }
-        tc_fence_after();
+        float* slot = scale_ring + s * S::kScaleFloats;
+        const float* sa = a.sa + size_t(kb) * a.M;
+        for (int i = lane; i < kLfBM; i += 32)
+          cp_async4(slot + i, w.m0 + i < a.M ? sa + w.m0 + i : sa, w.m0 + i < a.M);
+        if constexpr (ROWB) {
+          const float* sb = a.sb + size_t(kb) * a.N;
+          for (int i = lane; i < BN; i += 32)
+            cp_async4(slot + kLfBM + i, w.n0 + i < a.N ? sb + w.n0 + i : sb, w.n0 + i < a.N);
+        } else if (lane < BN / kFp8Block) {
+          const float* sb = a.sb + size_t(kb) * a.n_blocks;
+          const int n = w.n0 / kFp8Block + lane;
+          cp_async4(slot + kLfBM + lane, n < a.n_blocks ? sb + n : sb, n < a.n_blocks);
+        }
+        cp_async_arrive(&sfull[s]);
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp >= kLfFrontWarps) {
+    // ---- epilogue warps: TMEM lanes 32 (warp % 4) .. + 31, column quarter h ----
+    const int ew = warp - kLfFrontWarps, q = warp & 3, h = ew >> 2;
+    unsigned char* buf = store_buf + ew * kLfStoreBytes;
+    uint32_t it = 0;
+    bool stop = false;
+    for (int item = blockIdx.x; item < a.items && !stop; item += gridDim.x) {
+      const LinearItem w = linear_item<BN>(a, item);
+      const int col0 = w.n0 + h * kWide;
+      const int cols = min(kWide, a.N - col0);  // columns of this warp inside the tensor
+      // the sums start from the bias, spread over the lanes through the buffer
+      float2 acc[kWide / 2];
+      if (a.bias != nullptr) {
+        float* b = reinterpret_cast<float*>(buf);
+        __syncwarp();
+        for (int c = lane; c < kWide; c += 32) b[c] = c < cols ? __ldg(a.bias + col0 + c) : 0.f;
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < kWide / 2; ++i) acc[i] = *reinterpret_cast<const float2*>(b + 2 * i);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kWide / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+      }
+      for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
+        const int t = int(it % S::kAccs), s = int(it % kLfScaleSlots);
+        if (*abort_flag || !mbar_wait_bounded(&sfull[s], (it / kLfScaleSlots) & 1) ||
+            !mbar_wait_bounded(&tfull[t], (it / S::kAccs) & 1)) {
+          give_up();
+          stop = true;
+          break;
+        }
+        const float* slot = scale_ring + s * S::kScaleFloats;
+        float s_row = slot[q * 32 + lane];
+        if (!ROWB) s_row *= slot[kLfBM + h * kWide / kFp8Block];
         const float2 s2 = make_float2(s_row, s_row);
+        const float* s_col = slot + kLfBM + h * kWide;
+        tc_fence_after();
+        const uint32_t taddr =
+            tmem_base + (uint32_t(q * 32) << 16) + uint32_t(t * BN + h * kWide);
+        // chunks of 16 columns; the next one's load runs under this one's additions
+        // (columns behind the tensor's last are never stored)
+        uint32_t v[2][16];
+        if (cols > 0) {
+          tmem_ld16_async(taddr, v[0]);
 #pragma unroll
-        for (int c = 0; c < kHalf / 32; ++c) {
-          if (c * 32 >= cols) break;
-          float v[32];
-          tmem_ld32(tmem_base + (uint32_t(q * 32) << 16) + uint32_t(t * BN + h * kHalf + c * 32),
-                    v);
+          for (int c = 0; c < kWide / 16; ++c) {
+            tmem_wait16(v[c & 1]);
+            if (c + 1 < kWide / 16) tmem_ld16_async(taddr + uint32_t(c + 1) * 16, v[(c + 1) & 1]);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float2 sc = s2;
-            if constexpr (ROWB) {
-              const float2 cs = *reinterpret_cast<const float2*>(col_scale + c * 32 + 2 * i);
-              sc = __fmul2_rn(s2, cs);
+            for (int i = 0; i < 8; ++i) {
+              float2 sc = s2;
+              if constexpr (ROWB)
+                sc = __fmul2_rn(s2, *reinterpret_cast<const float2*>(s_col + c * 16 + 2 * i));
+              acc[c * 8 + i] = __ffma2_rn(make_float2(__uint_as_float(v[c & 1][2 * i]),
+                                                      __uint_as_float(v[c & 1][2 * i + 1])),
+                                          sc, acc[c * 8 + i]);
             }
-            acc[c * 16 + i] = __ffma2_rn(make_float2(v[2 * i], v[2 * i + 1]), sc, acc[c * 16 + i]);
           }
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&tempty[t]);
+        if (lane == 0) {
+          mbar_arrive(&tempty[t]);
+          mbar_arrive(&sempty[s]);
+        }
       }
       if (stop) break;
       // ---- the item's output: 32 rows x 128 bytes at a time ----
+      constexpr int kCols = 128 / int(sizeof(T)) < kWide ? 128 / int(sizeof(T)) : kWide;
+      constexpr int kPer = 16 / int(sizeof(T));
+      constexpr int kUnits = kCols / kPer;  // 16-byte units of a row: 8, or 4
+      const int r0 = w.m0 + q * 32;
+      const int rows = min(32, a.M - r0);
+      T* out = static_cast<T*>(a.out) + (size_t(w.split) * a.M + size_t(r0)) * a.out_pitch + col0;
+      const size_t total = size_t(a.splits) * a.M * a.out_pitch;
 #pragma unroll
-      for (int c = 0; c < kHalf / kCols; ++c) {
-        if (c * kCols >= cols) break;
-        if (lane == 0) bulk_wait_read0();
+      for (int c = 0; c < kWide / kCols; ++c) {
         __syncwarp();
 #pragma unroll
-        for (int g = 0; g < 8; ++g) {  // 16 bytes each
-          constexpr int kPer = 16 / int(sizeof(T));
+        for (int g = 0; g < kUnits; ++g) {
           float f[kPer];
 #pragma unroll
-          for (int i = 0; i < kPer; ++i) {
-            const int j = c * kCols + g * kPer + i;
-            f[i] = (j & 1) ? acc[j >> 1].y : acc[j >> 1].x;
-            if (a.bias != nullptr) f[i] += j < cols ? __ldg(a.bias + col0 + j) : 0.f;
+          for (int i = 0; i < kPer; i += 2) {
+            f[i] = acc[(c * kCols + g * kPer + i) / 2].x;
+            f[i + 1] = acc[(c * kCols + g * kPer + i) / 2].y;
           }
           uint32_t p[4];
           Storage<T>::pack(p, f);
           *reinterpret_cast<uint4*>(buf + lane * 128 + ((g ^ (lane & 7)) << 4)) =
               make_uint4(p[0], p[1], p[2], p[3]);
         }
-        if (a.tma_out) {
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0 && w.m0 + q * 32 < a.M) {
-            tma_store_3d(&omap, buf, col0 + c * kCols, w.m0 + q * 32, w.split);
-            bulk_commit();
+        __syncwarp();
+        if (a.vec_out) {
+          const int g = lane % kUnits, cv = c * kCols + g * kPer;  // this lane's 16 bytes
+          for (int r = lane / kUnits; r < rows; r += 32 / kUnits) {
+            const uint4 x = *reinterpret_cast<const uint4*>(buf + r * 128 + ((g ^ (r & 7)) << 4));
+            T* o = out + size_t(r) * a.out_pitch + cv;
+            if (cv < cols &&
+                in_range_of(a.error_word, size_t(o - static_cast<T*>(a.out)), kPer, total))
+              *reinterpret_cast<uint4*>(o) = x;
           }
         } else {
-          __syncwarp();
-          const int rows = min(32, a.M - (w.m0 + q * 32));
-          for (int r = 0; r < rows; ++r) {
-            const size_t o = (size_t(w.split) * a.M + size_t(w.m0 + q * 32 + r)) * a.out_pitch;
-#pragma unroll
-            for (int e = 0; e < kCols / 32; ++e) {
-              const int j = e * 32 + lane;  // column of the 128-byte row
-              const int byte = j * int(sizeof(T));
-              const T v = *reinterpret_cast<const T*>(buf + r * 128 +
-                                                      (((byte >> 4) ^ (r & 7)) << 4) + (byte & 15));
-              if (c * kCols + j < cols &&
-                  in_range_of(a.error_word, o + col0 + c * kCols + j, 1,
-                              size_t(a.splits) * a.M * a.out_pitch))
-                static_cast<T*>(a.out)[o + col0 + c * kCols + j] = v;
-            }
+          for (int e = lane; e < rows * kCols; e += 32) {
+            const int r = e / kCols, j = e % kCols, byte = j * int(sizeof(T));
+            const T x = *reinterpret_cast<const T*>(
+                buf + r * 128 + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 15));
+            T* o = out + size_t(r) * a.out_pitch + c * kCols + j;
+            if (c * kCols + j < cols &&
+                in_range_of(a.error_word, size_t(o - static_cast<T*>(a.out)), 1, total))
+              *o = x;
           }
-          __syncwarp();
         }
       }
     }
-    if (lane == 0) bulk_wait0();
   }
 
   tc_fence_before();
