@@ -9,6 +9,7 @@
 
 #include <algorithm>
 #include <climits>
+#include <cstring>
 
 #include "dcn_fp8.cuh"
 #include "dcn_host.h"
@@ -125,15 +126,38 @@ dcn_status codes_map(CUtensorMap* map, const void* base, int inner, int64_t pitc
   return cr == CUDA_SUCCESS ? DCN_OK : DCN_ERR_UNSUPPORTED;
 }
 
+// 3-D map (columns, rows, splits) of the output; the box is what an epilogue warp
+// stores at once: 32 rows of a quarter of the column tile, 128 bytes at most.
+dcn_status out_map(CUtensorMap* map, void* base, dcn_dtype dtype, int N, int pitch, int M,
+                   int splits, int bn) {
+  const int e = esize(dtype), width = std::min(128 / e, bn / 4);
+  const cuuint64_t dims[3] = {cuuint64_t(N), cuuint64_t(M), cuuint64_t(splits)};
+  const cuuint64_t strides[2] = {cuuint64_t(pitch) * e, cuuint64_t(pitch) * e * cuuint64_t(M)};
+  const cuuint32_t box[3] = {cuuint32_t(width), 32u, 1u};
+  const cuuint32_t estr[3] = {1u, 1u, 1u};
+  const CUresult cr = tensor_map_encoder()(
+      map,
+      dtype == DCN_BF16  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+      : dtype == DCN_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                         : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+      3, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+      width * e == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+      CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return cr == CUDA_SUCCESS ? DCN_OK : DCN_ERR_UNSUPPORTED;
+}
+
 template <typename T, int BN, bool ROWB>
-dcn_status launch_linear(const CUtensorMap& amap, const CUtensorMap& bmap, const LinearArgs& args,
-                         int sms, cudaStream_t stream) {
+dcn_status launch_linear(const CUtensorMap& amap, const CUtensorMap& bmap, const CUtensorMap& omap,
+                         LinearArgs args, int sms, cudaStream_t stream) {
   auto k = dcn_linear_fp8_kernel<T, BN, ROWB>;
   constexpr size_t smem = LfShape<BN>::kSmemBytes;
   if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) !=
       cudaSuccess)
     return DCN_ERR_CUDA;
-  k<<<unsigned(std::min(args.items, sms)), kLfThreads, smem, stream>>>(amap, bmap, args);
+  const int grid = std::min(args.items, sms);
+  args.step_n = grid % args.n_tiles;
+  args.step_m = grid / args.n_tiles;
+  k<<<unsigned(grid), kLfThreads, smem, stream>>>(amap, bmap, omap, args);
   return launched();
 }
 
@@ -183,19 +207,22 @@ dcn_status linear(const void* a, const float* sa, int M, int K, const void* b, c
   g.bias = split ? nullptr : bias;
   g.out = split ? workspace : out;
   g.out_pitch = split ? p.part_pitch : N;
-  g.vec_out = (int64_t(g.out_pitch) * esize(kernel_dtype)) % 16 == 0;
+  g.tma_out = (int64_t(g.out_pitch) * esize(kernel_dtype)) % 16 == 0;
   g.error_word = dev.error_word;
-  CUtensorMap amap, bmap;
+  CUtensorMap amap, bmap, omap;
+  std::memset(&omap, 0, sizeof(omap));
   dcn_status st;
   if ((st = codes_map(&amap, a, K, pitch, M, kLfBM)) != DCN_OK) return st;
   if ((st = codes_map(&bmap, b, K, pitch, N, p.bn)) != DCN_OK) return st;
+  if (g.tma_out && (st = out_map(&omap, g.out, kernel_dtype, N, g.out_pitch, M, p.splits, p.bn)) != DCN_OK)
+    return st;
   st = with_storage(kernel_dtype, [&](auto tag) {
     using T = decltype(tag);
     if (row_scales)
-      return p.bn == 256 ? launch_linear<T, 256, true>(amap, bmap, g, dev.sms, stream)
-                         : launch_linear<T, 128, true>(amap, bmap, g, dev.sms, stream);
-    return p.bn == 256 ? launch_linear<T, 256, false>(amap, bmap, g, dev.sms, stream)
-                       : launch_linear<T, 128, false>(amap, bmap, g, dev.sms, stream);
+      return p.bn == 256 ? launch_linear<T, 256, true>(amap, bmap, omap, g, dev.sms, stream)
+                         : launch_linear<T, 128, true>(amap, bmap, omap, g, dev.sms, stream);
+    return p.bn == 256 ? launch_linear<T, 256, false>(amap, bmap, omap, g, dev.sms, stream)
+                       : launch_linear<T, 128, false>(amap, bmap, omap, g, dev.sms, stream);
   });
   if (st != DCN_OK || !split) return st;
   return with_storage(out_dtype, [&](auto tag) {

@@ -12,10 +12,10 @@
 // fastest (the row tile of A stays in L2 while B's column tiles pass).  Warp 0
 // streams 128-byte K blocks of A and B into a shared-memory ring by TMA (128-byte
 // swizzle); one thread of warp 1 issues tcgen05.mma (kind::f8f6f4, K = 32) for one
-// block at a time into one of 512 / BN accumulators; warp 2 brings the blocks'
-// scales into a ring of their own with asynchronous copies; sixteen epilogue warps
+// block at a time into one of 512 / BN accumulators; warp 2 brings the blocks' scales
+// into a ring of their own with asynchronous copies; sixteen epilogue warps
 // (four lane quarters x four column quarters) read each accumulator back, scale and
-// add it, and at an item's end store it through a swizzled 4 KB buffer each.  The
+// add it, and at an item's end store it by TMA from a swizzled 4 KB buffer each.  The
 // sums of a 128 x 256 tile take 64 of the 96 registers of every epilogue thread, and
 // four epilogue warps a scheduler hide each other's tensor-memory reads.  (Eight
 // warps with 128 sums a thread spill, with or without registers moved to them.)
@@ -38,6 +38,7 @@ constexpr int kLfEpiWarps = 16;
 constexpr int kLfThreads = (kLfFrontWarps + kLfEpiWarps) * 32;
 constexpr uint32_t kLfTmemCols = 512;
 constexpr int kLfStoreBytes = 32 * 128;  // an epilogue warp's buffer: 32 rows of 128 bytes
+constexpr int kLfBiasBytes = 64 * 4;     // and its columns' bias
 constexpr int kLfScaleSlots = 4;         // K blocks whose scales are in flight
 
 template <int BN>
@@ -47,9 +48,9 @@ struct LfShape {
   static constexpr uint32_t kStageBytes = uint32_t(kLfBM + BN) * kLfBK;
   static constexpr int kScaleFloats = kLfBM + BN;  // a slot: row scales, column scales
   static constexpr size_t kSmemBytes = 1024 /* alignment slack */ + size_t(kStages) * kStageBytes +
-                                       size_t(kLfEpiWarps) * kLfStoreBytes +
+                                       size_t(kLfEpiWarps) * (kLfStoreBytes + kLfBiasBytes) +
                                        size_t(kLfScaleSlots) * kScaleFloats * 4 +
-                                       256 /* barriers, TMEM address */;
+                                       512 /* barriers, TMEM address */;
 };
 
 struct LinearArgs {
@@ -58,13 +59,14 @@ struct LinearArgs {
   int m_tiles, n_tiles;
   int splits, kb_per;      // K splits and blocks of each (the last may have fewer)
   int items;               // m_tiles * n_tiles * splits
+  int step_n, step_m;      // CTAs % n_tiles and CTAs / n_tiles: from one item of a CTA to its next
   int n_blocks;            // ceil(N / 128): pitch of sb with blocks of 128 rows
   const float* sa;         // (k_blocks, M)
   const float* sb;         // (k_blocks, n_blocks), or (k_blocks, N) with a scale a row
   const float* bias;       // N values, or null
   void* out;               // (splits, M, out_pitch) values of the output type
   int out_pitch;
-  int vec_out;             // 1: rows start on 16-byte boundaries: vector stores
+  int tma_out;             // 1: rows are multiples of 16 bytes, stored by TMA
   unsigned int* error_word;
 };
 
@@ -107,6 +109,59 @@ __device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
                : "memory");
 }
 
+// A ring of `N` barriers as one role walks it: the current slot and its phase, without
+// a division a step (the roles are single threads or warps whose instructions stand
+// in the accumulators' round trip).
+template <int N>
+struct RingPos {
+  uint32_t slot = 0, phase;
+  __device__ __forceinline__ explicit RingPos(uint32_t first_phase) : phase(first_phase) {}
+  __device__ __forceinline__ void next() {
+    if (++slot == uint32_t(N)) {
+      slot = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
+// The part of a wait that did not succeed at once: gives up after 2^31 cycles (about
+// a second), or soon after another role has (abort_flag).
+__device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  const long long t0 = clock64();
+#pragma unroll 1
+  for (uint32_t i = 1; i < (1u << 28); ++i) {
+    if (mbar_try(bar, parity)) return true;
+    if ((i & 63u) == 0 && (*abort_flag || clock64() - t0 > (1ll << 31))) return false;
+  }
+  return false;
+}
+
+// Bounded wait of this kernel's roles.
+__device__ __forceinline__ bool mbar_wait_watch(uint32_t bar, uint32_t parity,
+                                                volatile int* abort_flag) {
+  if (mbar_try(bar, parity)) return true;
+  return mbar_wait_long(bar, parity, abort_flag);
+}
+
+__device__ __forceinline__ void mbar_arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void umma_commit_at(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+               : "memory");
+}
+
 // An asynchronous 4-byte copy to shared memory; zero where `in` is false.
 __device__ __forceinline__ void cp_async4(float* dst, const float* src, bool in) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_addr(dst)), "l"(src),
@@ -119,28 +174,70 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
                : "memory");
 }
 
-struct LinearItem {
-  int m0, n0, split, kb0, kb1;
-};
-
-template <int BN>
-__device__ __forceinline__ LinearItem linear_item(const LinearArgs& a, int item) {
-  LinearItem i;
-  const int nt = item % a.n_tiles, r = item / a.n_tiles;
-  i.split = r / a.m_tiles;
-  i.m0 = (r - i.split * a.m_tiles) * kLfBM;
-  i.n0 = nt * BN;
-  i.kb0 = i.split * a.kb_per;
-  i.kb1 = min(i.kb0 + a.kb_per, a.k_blocks);
-  return i;
+// Stores a box from shared memory; rows and columns outside the tensor are left out.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int c0,
+                                             int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(smem_addr(src)), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
 }
+__device__ __forceinline__ void bulk_commit() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// The thread's stores have been read from shared memory (read0), or are complete.
+__device__ __forceinline__ void bulk_wait_read0() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_wait0() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
+// A CTA's items blockIdx.x, blockIdx.x + gridDim.x, ...: column tile fastest, then
+// row tile, then K split.  Moving on adds the grid's steps; no division after the first.
+template <int BN>
+struct LinearItems {
+  int item, nt, mt, split;
+  int m0, n0, kb0, kb1;
+  __device__ __forceinline__ explicit LinearItems(const LinearArgs& a) {
+    item = int(blockIdx.x);
+    const int r = item / a.n_tiles;
+    nt = item - r * a.n_tiles;
+    split = r / a.m_tiles;
+    mt = r - split * a.m_tiles;
+    place(a);
+  }
+  __device__ __forceinline__ bool valid(const LinearArgs& a) const { return item < a.items; }
+  __device__ __forceinline__ void next(const LinearArgs& a) {
+    item += int(gridDim.x);
+    nt += a.step_n;
+    mt += a.step_m;
+    if (nt >= a.n_tiles) {
+      nt -= a.n_tiles;
+      ++mt;
+    }
+    while (mt >= a.m_tiles) {
+      mt -= a.m_tiles;
+      ++split;
+    }
+    place(a);
+  }
+  __device__ __forceinline__ void place(const LinearArgs& a) {
+    m0 = mt * kLfBM;
+    n0 = nt * BN;
+    kb0 = split * a.kb_per;
+    kb1 = min(kb0 + a.kb_per, a.k_blocks);
+  }
+};
 
 // T: output type.  BN: column tile.  ROWB: sb holds a scale for each row of B (the
 // weight gradient), else one for each 128 rows.
 template <typename T, int BN, bool ROWB>
 __global__ void __launch_bounds__(kLfThreads, 1)
     dcn_linear_fp8_kernel(const __grid_constant__ CUtensorMap amap,
-                          const __grid_constant__ CUtensorMap bmap, const LinearArgs a) {
+                          const __grid_constant__ CUtensorMap bmap,
+                          const __grid_constant__ CUtensorMap omap, const LinearArgs a) {
   using S = LfShape<BN>;
   constexpr int kWide = BN / 4;  // columns of an epilogue warp
   extern __shared__ __align__(1024) unsigned char lf_smem_raw[];
@@ -148,10 +245,11 @@ __global__ void __launch_bounds__(kLfThreads, 1)
   unsigned char* stage_a = smem;
   unsigned char* stage_b = smem + size_t(S::kStages) * kLfBM * kLfBK;
   unsigned char* store_buf = smem + size_t(S::kStages) * S::kStageBytes;
-  float* scale_ring = reinterpret_cast<float*>(store_buf + kLfEpiWarps * kLfStoreBytes);
+  float* bias_buf = reinterpret_cast<float*>(store_buf + kLfEpiWarps * kLfStoreBytes);
+  float* scale_ring = bias_buf + kLfEpiWarps * kLfBiasBytes / 4;
   uint64_t* full = reinterpret_cast<uint64_t*>(scale_ring + kLfScaleSlots * S::kScaleFloats);
   uint64_t* empty = full + S::kStages;
-  uint64_t* tfull = empty + S::kStages;   // accumulator ready
+  uint64_t* tfull = empty + S::kStages;       // accumulator ready
   uint64_t* tempty = tfull + S::kAccs;    // accumulator read
   uint64_t* sfull = tempty + S::kAccs;    // scales landed
   uint64_t* sempty = sfull + kLfScaleSlots;
@@ -194,58 +292,62 @@ __global__ void __launch_bounds__(kLfThreads, 1)
     *abort_flag = 1;
   };
 
+  const uint32_t full_a = smem_addr(full), empty_a = smem_addr(empty), tfull_a = smem_addr(tfull),
+                 tempty_a = smem_addr(tempty), sfull_a = smem_addr(sfull),
+                 sempty_a = smem_addr(sempty);
+  // A wait on the phase before a barrier's first succeeds at once: rings start
+  // empty, so whoever fills them starts with phase 1 and whoever drains them with 0.
   if (warp == 0) {
     // ---- TMA producer ----
     if (lane == 0) {
-      uint32_t it = 0;
+      RingPos<S::kStages> r(1);
+      uint32_t issued = 0;
       bool stop = false;
-      for (int item = blockIdx.x; item < a.items && !stop; item += gridDim.x) {
-        const LinearItem w = linear_item<BN>(a, item);
-        for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
-          if (*abort_flag) { stop = true; break; }
-          const int s = int(it % S::kStages);
-          const uint32_t u = it / S::kStages;
-          if (u > 0 && !mbar_wait_bounded(&empty[s], (u - 1) & 1)) {
+      for (LinearItems<BN> w(a); w.valid(a) && !stop; w.next(a)) {
+        for (int kb = w.kb0; kb < w.kb1; ++kb, r.next(), ++issued) {
+          if (!mbar_wait_watch(empty_a + 8 * r.slot, r.phase, abort_flag)) {
             give_up();
             stop = true;
             break;
           }
-          mbar_arrive_expect_tx(&full[s], S::kStageBytes);
-          tma_load_2d(stage_a + size_t(s) * kLfBM * kLfBK, &amap, &full[s], kb * kLfBK, w.m0);
-          tma_load_2d(stage_b + size_t(s) * BN * kLfBK, &bmap, &full[s], kb * kLfBK, w.n0);
+          mbar_arrive_expect_tx(&full[r.slot], S::kStageBytes);
+          tma_load_2d(stage_a + r.slot * (kLfBM * kLfBK), &amap, &full[r.slot], kb * kLfBK, w.m0);
+          tma_load_2d(stage_b + r.slot * (BN * kLfBK), &bmap, &full[r.slot], kb * kLfBK, w.n0);
         }
       }
       // the copies of the last issued stages may still be landing
-      for (uint32_t j = it > uint32_t(S::kStages) ? it - S::kStages : 0; j < it; ++j)
+      for (uint32_t j = issued > uint32_t(S::kStages) ? issued - S::kStages : 0; j < issued; ++j)
         (void)mbar_wait_bounded(&full[j % S::kStages], (j / S::kStages) & 1);
     }
   } else if (warp == 1) {
     // ---- MMA issuer: one K block, one accumulator ----
     if (lane == 0) {
-      uint32_t it = 0;
+      RingPos<S::kStages> r(0);
+      RingPos<S::kAccs> t(1);
+      const uint64_t a_desc0 = umma_desc_sw128(smem_addr(stage_a));
+      const uint64_t b_desc0 = umma_desc_sw128(smem_addr(stage_b));
       bool stop = false;
-      for (int item = blockIdx.x; item < a.items && !stop; item += gridDim.x) {
-        const LinearItem w = linear_item<BN>(a, item);
+      for (LinearItems<BN> w(a); w.valid(a) && !stop; w.next(a)) {
         const uint32_t idesc = umma_idesc_e4m3_f32(kLfBM, min(BN, (a.N - w.n0 + 15) / 16 * 16));
-        for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
-          const int acc = int(it % S::kAccs), s = int(it % S::kStages);
-          const uint32_t ua = it / S::kAccs;
-          if (*abort_flag || (ua > 0 && !mbar_wait_bounded(&tempty[acc], (ua - 1) & 1)) ||
-              !mbar_wait_bounded(&full[s], (it / S::kStages) & 1)) {
+        for (int kb = w.kb0; kb < w.kb1; ++kb, r.next(), t.next()) {
+          if (!mbar_wait_watch(full_a + 8 * r.slot, r.phase, abort_flag) ||
+              !mbar_wait_watch(tempty_a + 8 * t.slot, t.phase, abort_flag)) {
             give_up();
             stop = true;
             break;
           }
           tc_fence_after();
-          const uint32_t d = tmem_base + uint32_t(acc * BN);
-          const uint32_t a_addr = smem_addr(stage_a + size_t(s) * kLfBM * kLfBK);
-          const uint32_t b_addr = smem_addr(stage_b + size_t(s) * BN * kLfBK);
-          const int steps = min(4, (a.K - kb * kLfBK + 31) / 32);  // bytes behind K are zeros
-          for (int k = 0; k < steps; ++k)
-            umma_e4m3(d, umma_desc_sw128(a_addr + 32 * k), umma_desc_sw128(b_addr + 32 * k), idesc,
-                      uint32_t(k != 0));
-          umma_commit(&empty[s]);
-          umma_commit(&tfull[acc]);
+          // 32 bytes of K an instruction (2 units of 16 in a descriptor's address)
+          const uint64_t ad = a_desc0 + r.slot * (kLfBM * kLfBK / 16);
+          const uint64_t bd = b_desc0 + r.slot * (BN * kLfBK / 16);
+          const uint32_t d = tmem_base + t.slot * BN;
+          umma_e4m3(d, ad, bd, idesc, 0);
+          const int left = a.K - kb * kLfBK;  // bytes behind K are zeros: no need to multiply them
+          if (left > 32) umma_e4m3(d, ad + 2, bd + 2, idesc, 1);
+          if (left > 64) umma_e4m3(d, ad + 4, bd + 4, idesc, 1);
+          if (left > 96) umma_e4m3(d, ad + 6, bd + 6, idesc, 1);
+          umma_commit_at(tfull_a + 8 * t.slot);
+          umma_commit_at(empty_a + 8 * r.slot);
         }
       }
       // every MMA issued has retired before the accumulators are freed
@@ -254,24 +356,23 @@ __global__ void __launch_bounds__(kLfThreads, 1)
     }
   } else if (warp == 2) {
     // ---- scales ----
-    uint32_t it = 0;
+    RingPos<kLfScaleSlots> r(1);
     bool stop = false;
-    for (int item = blockIdx.x; item < a.items && !stop; item += gridDim.x) {
-      const LinearItem w = linear_item<BN>(a, item);
-      for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
-        const int s = int(it % kLfScaleSlots);
-        const uint32_t u = it / kLfScaleSlots;
-        if (*abort_flag || (u > 0 && !mbar_wait_bounded(&sempty[s], (u - 1) & 1))) {
+    for (LinearItems<BN> w(a); w.valid(a) && !stop; w.next(a)) {
+      for (int kb = w.kb0; kb < w.kb1; ++kb, r.next()) {
+        if (!mbar_wait_watch(sempty_a + 8 * r.slot, r.phase, abort_flag)) {
           give_up();
           stop = true;
           break;
         }
-        float* slot = scale_ring + s * S::kScaleFloats;
+        float* slot = scale_ring + r.slot * S::kScaleFloats;
         const float* sa = a.sa + size_t(kb) * a.M;
+#pragma unroll
         for (int i = lane; i < kLfBM; i += 32)
           cp_async4(slot + i, w.m0 + i < a.M ? sa + w.m0 + i : sa, w.m0 + i < a.M);
         if constexpr (ROWB) {
           const float* sb = a.sb + size_t(kb) * a.N;
+#pragma unroll
           for (int i = lane; i < BN; i += 32)
             cp_async4(slot + kLfBM + i, w.n0 + i < a.N ? sb + w.n0 + i : sb, w.n0 + i < a.N);
         } else if (lane < BN / kFp8Block) {
@@ -279,7 +380,7 @@ __global__ void __launch_bounds__(kLfThreads, 1)
           const int n = w.n0 / kFp8Block + lane;
           cp_async4(slot + kLfBM + lane, n < a.n_blocks ? sb + n : sb, n < a.n_blocks);
         }
-        cp_async_arrive(&sfull[s]);
+        cp_async_arrive(&sfull[r.slot]);
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -287,79 +388,112 @@ __global__ void __launch_bounds__(kLfThreads, 1)
     // ---- epilogue warps: TMEM lanes 32 (warp % 4) .. + 31, column quarter h ----
     const int ew = warp - kLfFrontWarps, q = warp & 3, h = ew >> 2;
     unsigned char* buf = store_buf + ew * kLfStoreBytes;
-    uint32_t it = 0;
+    float* bias_w = bias_buf + ew * kLfBiasBytes / 4;
+    const uint32_t tq = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(h * kWide);
+    const float* row_scale = scale_ring + q * 32 + lane;
+    const float* col_scale = scale_ring + kLfBM + (ROWB ? h * kWide : h * kWide / kFp8Block);
+    constexpr int kLanes = kWide / 32;  // columns of a lane when the bias is fetched
+    float bias[kLanes];
+    LinearItems<BN> w(a);
+    auto fetch_bias = [&]() {
+      if (a.bias == nullptr || !w.valid(a)) return;
+#pragma unroll
+      for (int i = 0; i < kLanes; ++i) {
+        const int c = w.n0 + h * kWide + i * 32 + lane;
+        bias[i] = c < a.N ? __ldg(a.bias + c) : 0.f;
+      }
+    };
+    fetch_bias();
+    RingPos<S::kAccs> t(0);
+    RingPos<kLfScaleSlots> sr(0);
+    // The row's scale of a K block (times the block's; column scales stay in the ring).
+    float s_next = 0.f;
+    auto read_scale = [&]() {
+      if (mbar_wait_watch(sfull_a + 8 * sr.slot, sr.phase, abort_flag)) {
+        s_next = row_scale[sr.slot * S::kScaleFloats];
+        if (!ROWB) s_next *= col_scale[sr.slot * S::kScaleFloats];
+      }
+    };
     bool stop = false;
-    for (int item = blockIdx.x; item < a.items && !stop; item += gridDim.x) {
-      const LinearItem w = linear_item<BN>(a, item);
+    while (w.valid(a) && !stop) {
       const int col0 = w.n0 + h * kWide;
       const int cols = min(kWide, a.N - col0);  // columns of this warp inside the tensor
-      // the sums start from the bias, spread over the lanes through the buffer
+      const int r0 = w.m0 + q * 32, split = w.split;
+      const int kbs = w.kb1 - w.kb0;
+      // the sums start from the bias, spread over the lanes through shared memory
       float2 acc[kWide / 2];
       if (a.bias != nullptr) {
-        float* b = reinterpret_cast<float*>(buf);
-        __syncwarp();
-        for (int c = lane; c < kWide; c += 32) b[c] = c < cols ? __ldg(a.bias + col0 + c) : 0.f;
+#pragma unroll
+        for (int i = 0; i < kLanes; ++i) bias_w[i * 32 + lane] = bias[i];
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < kWide / 2; ++i) acc[i] = *reinterpret_cast<const float2*>(b + 2 * i);
+        for (int i = 0; i < kWide / 4; ++i) {
+          const float4 b = *reinterpret_cast<const float4*>(bias_w + 4 * i);
+          acc[2 * i] = make_float2(b.x, b.y);
+          acc[2 * i + 1] = make_float2(b.z, b.w);
+        }
       } else {
 #pragma unroll
         for (int i = 0; i < kWide / 2; ++i) acc[i] = make_float2(0.f, 0.f);
       }
-      for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
-        const int t = int(it % S::kAccs), s = int(it % kLfScaleSlots);
-        if (*abort_flag || !mbar_wait_bounded(&sfull[s], (it / kLfScaleSlots) & 1) ||
-            !mbar_wait_bounded(&tfull[t], (it / S::kAccs) & 1)) {
+      w.next(a);
+      fetch_bias();
+      for (int kb = 0; kb < kbs; ++kb, t.next(), sr.next()) {
+        read_scale(); const float2 s2 = make_float2(s_next, s_next);
+        const float* s_col = col_scale + sr.slot * S::kScaleFloats;
+        const uint32_t s_done = sempty_a + 8 * sr.slot;
+        if (!mbar_wait_watch(tfull_a + 8 * t.slot, t.phase, abort_flag)) {
           give_up();
           stop = true;
           break;
         }
-        const float* slot = scale_ring + s * S::kScaleFloats;
-        float s_row = slot[q * 32 + lane];
-        if (!ROWB) s_row *= slot[kLfBM + h * kWide / kFp8Block];
-        const float2 s2 = make_float2(s_row, s_row);
-        const float* s_col = slot + kLfBM + h * kWide;
         tc_fence_after();
-        const uint32_t taddr =
-            tmem_base + (uint32_t(q * 32) << 16) + uint32_t(t * BN + h * kWide);
         // chunks of 16 columns; the next one's load runs under this one's additions
         // (columns behind the tensor's last are never stored)
         uint32_t v[2][16];
-        if (cols > 0) {
-          tmem_ld16_async(taddr, v[0]);
+        tmem_ld16_async(tq + t.slot * BN, v[0]);
 #pragma unroll
-          for (int c = 0; c < kWide / 16; ++c) {
-            tmem_wait16(v[c & 1]);
-            if (c + 1 < kWide / 16) tmem_ld16_async(taddr + uint32_t(c + 1) * 16, v[(c + 1) & 1]);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              float2 sc = s2;
-              if constexpr (ROWB)
-                sc = __fmul2_rn(s2, *reinterpret_cast<const float2*>(s_col + c * 16 + 2 * i));
-              acc[c * 8 + i] = __ffma2_rn(make_float2(__uint_as_float(v[c & 1][2 * i]),
-                                                      __uint_as_float(v[c & 1][2 * i + 1])),
-                                          sc, acc[c * 8 + i]);
+        for (int c = 0; c < kWide / 16; ++c) {
+          tmem_wait16(v[c & 1]);
+          if (c + 1 < kWide / 16) {
+            tmem_ld16_async(tq + t.slot * BN + (c + 1) * 16, v[(c + 1) & 1]);
+          } else {  // all read: the accumulator may be overwritten
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive_at(tempty_a + 8 * t.slot);
+              if (!ROWB) mbar_arrive_at(s_done);
             }
           }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float2 sc = s2;
+            if constexpr (ROWB)
+              sc = __fmul2_rn(s2, *reinterpret_cast<const float2*>(s_col + c * 16 + 2 * i));
+            acc[c * 8 + i] = __ffma2_rn(make_float2(__uint_as_float(v[c & 1][2 * i]),
+                                                    __uint_as_float(v[c & 1][2 * i + 1])),
+                                        sc, acc[c * 8 + i]);
+          }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&tempty[t]);
-          mbar_arrive(&sempty[s]);
+        if (ROWB) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive_at(s_done);
         }
       }
       if (stop) break;
-      // ---- the item's output: 32 rows x 128 bytes at a time ----
+      // ---- the item's output: 32 rows of up to 128 bytes at a time ----
       constexpr int kCols = 128 / int(sizeof(T)) < kWide ? 128 / int(sizeof(T)) : kWide;
       constexpr int kPer = 16 / int(sizeof(T));
-      constexpr int kUnits = kCols / kPer;  // 16-byte units of a row: 8, or 4
-      const int r0 = w.m0 + q * 32;
+      constexpr int kUnits = kCols / kPer;      // 16-byte units of a row: 8, or 4
+      constexpr int kRowBytes = kUnits * 16;
+      // the 128- or 64-byte swizzle of the output's tensor map
+      auto unit_at = [](int r, int g) {
+        return r * kRowBytes + ((kUnits == 8 ? g ^ (r & 7) : g ^ ((r >> 1) & 3)) << 4);
+      };
       const int rows = min(32, a.M - r0);
-      T* out = static_cast<T*>(a.out) + (size_t(w.split) * a.M + size_t(r0)) * a.out_pitch + col0;
-      const size_t total = size_t(a.splits) * a.M * a.out_pitch;
 #pragma unroll
       for (int c = 0; c < kWide / kCols; ++c) {
+        if (lane == 0) bulk_wait_read0();  // the buffer's last store has been read
         __syncwarp();
 #pragma unroll
         for (int g = 0; g < kUnits; ++g) {
@@ -371,32 +505,30 @@ __global__ void __launch_bounds__(kLfThreads, 1)
           }
           uint32_t p[4];
           Storage<T>::pack(p, f);
-          *reinterpret_cast<uint4*>(buf + lane * 128 + ((g ^ (lane & 7)) << 4)) =
-              make_uint4(p[0], p[1], p[2], p[3]);
+          *reinterpret_cast<uint4*>(buf + unit_at(lane, g)) = make_uint4(p[0], p[1], p[2], p[3]);
         }
-        __syncwarp();
-        if (a.vec_out) {
-          const int g = lane % kUnits, cv = c * kCols + g * kPer;  // this lane's 16 bytes
-          for (int r = lane / kUnits; r < rows; r += 32 / kUnits) {
-            const uint4 x = *reinterpret_cast<const uint4*>(buf + r * 128 + ((g ^ (r & 7)) << 4));
-            T* o = out + size_t(r) * a.out_pitch + cv;
-            if (cv < cols &&
-                in_range_of(a.error_word, size_t(o - static_cast<T*>(a.out)), kPer, total))
-              *reinterpret_cast<uint4*>(o) = x;
+        if (a.tma_out) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && rows > 0 && c * kCols < cols) {
+            tma_store_3d(&omap, buf, col0 + c * kCols, r0, split);
+            bulk_commit();
           }
         } else {
+          __syncwarp();
+          const size_t out0 = (size_t(split) * a.M + size_t(r0)) * a.out_pitch + col0 + c * kCols;
           for (int e = lane; e < rows * kCols; e += 32) {
             const int r = e / kCols, j = e % kCols, byte = j * int(sizeof(T));
-            const T x = *reinterpret_cast<const T*>(
-                buf + r * 128 + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 15));
-            T* o = out + size_t(r) * a.out_pitch + c * kCols + j;
+            const T x = *reinterpret_cast<const T*>(buf + unit_at(r, byte >> 4) + (byte & 15));
+            const size_t o = out0 + size_t(r) * a.out_pitch + j;
             if (c * kCols + j < cols &&
-                in_range_of(a.error_word, size_t(o - static_cast<T*>(a.out)), 1, total))
-              *o = x;
+                in_range_of(a.error_word, o, 1, size_t(a.splits) * a.M * a.out_pitch))
+              static_cast<T*>(a.out)[o] = x;
           }
         }
       }
     }
+    if (lane == 0) bulk_wait0();
   }
 
   tc_fence_before();
