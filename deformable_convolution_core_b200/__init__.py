@@ -379,45 +379,76 @@ def dcn_core_linear_bf16(input, M: int, K: int, weight, Nout: int, bias, output,
         int(out_dtype), _stream(stream)), "dcn_core_linear_bf16")
 
 
-def _torch_dtype(dtype: int) -> str:
-    return {DCN_F32: "torch.float32", DCN_BF16: "torch.bfloat16", DCN_F16: "torch.float16"}.get(
-        dtype, "")
+# Torch types by dcn_dtype, and those a buffer of e4m3 codes may have: filled when the
+# first tensor comes (the binding itself does not need torch).
+_TORCH: dict = {}
 
 
-_CODES = ("torch.float8_e4m3fn", "torch.uint8")  # types a buffer of e4m3 codes may have
+def _torch_types() -> dict:
+    if not _TORCH:
+        import torch
+        _TORCH.update({DCN_F32: (torch.float32,), DCN_BF16: (torch.bfloat16,),
+                       DCN_F16: (torch.float16,), "codes": (torch.float8_e4m3fn, torch.uint8),
+                       "device": torch.cuda.current_device,
+                       "stream": torch.cuda.current_stream,
+                       "raw_stream": getattr(torch._C, "_cuda_getCurrentRawStream", None)})
+    return _TORCH
 
 
-def _arg(t, name: str, numel: int, dtypes) -> int | None:
-    """The address of one argument of the block operators.  A torch tensor must be
-    contiguous, on the current device, of one of `dtypes` and of exactly `numel`
-    elements (a program that passes another size has mixed two tensors up); None
-    and raw addresses go through as they are."""
-    if t is None or isinstance(t, int):
-        return t
+def _bad_arg(t, name: str, numel: int, dtypes):
     if not hasattr(t, "data_ptr"):
         raise TypeError(f"{name}: cannot pass {type(t)} as a pointer")
     if not t.is_contiguous():
         raise ValueError(f"{name}: tensors passed to the C ABI must be contiguous")
-    import torch
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+    if not t.is_cuda or t.get_device() != _torch_types()["device"]():
         raise ValueError(f"{name}: the tensor is on {t.device}, not on the current CUDA device")
-    if str(t.dtype) not in dtypes:
-        raise ValueError(f"{name}: expected {' or '.join(dtypes)}, got {t.dtype}")
-    if t.numel() != numel:
-        raise ValueError(f"{name}: expected {numel} elements, got {t.numel()}")
-    return t.data_ptr()
+    if dtypes is not None and t.dtype not in dtypes:
+        raise ValueError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    raise ValueError(f"{name}: expected {numel} elements, got {t.numel()}")
 
 
-def _workspace_arg(t, nbytes: int) -> int | None:
-    if t is not None and hasattr(t, "data_ptr"):
+class _Args:
+    """Checks and converts the tensors of one call of the block operators: each must
+    be contiguous, on the current device, of the named type and of exactly the
+    number of elements that the sizes give (another size means that two tensors
+    were mixed up).  None and raw addresses go through as they are."""
+    __slots__ = ("types", "device")
+
+    def __init__(self):
+        self.types = _torch_types()
+        self.device = None
+
+    def __call__(self, t, name: str, numel: int, kind) -> int | None:
+        if t is None or type(t) is int:
+            return t
+        dtypes = self.types.get(kind)
+        try:
+            if self.device is None and t.is_cuda:
+                self.device = self.types["device"]()
+            if (t.dtype in dtypes and t.numel() == numel and t.is_cuda
+                    and t.get_device() == self.device and t.is_contiguous()):
+                return t.data_ptr()
+        except (AttributeError, TypeError):
+            pass
+        _bad_arg(t, name, numel, dtypes or ())
+
+    def workspace(self, t, nbytes: int) -> int | None:
+        if t is None or type(t) is int:
+            return t
         if t.numel() * t.element_size() < nbytes:
             raise ValueError(f"workspace: {nbytes} bytes named, the tensor has "
                              f"{t.numel() * t.element_size()}")
-        return _arg(t, "workspace", t.numel(), (str(t.dtype),))
-    return t
+        if not t.is_contiguous() or not t.is_cuda or t.get_device() != self.types["device"]():
+            _bad_arg(t, "workspace", t.numel(), None)
+        return t.data_ptr()
 
-
-_F32 = ("torch.float32",)
+    def stream(self, s) -> int | None:
+        if s is not None:
+            return s if type(s) is int else s.cuda_stream
+        raw = self.types["raw_stream"]
+        if raw is not None:
+            return raw(self.types["device"]() if self.device is None else self.device)
+        return self.types["stream"]().cuda_stream
 
 
 def _ceil(a: int, b: int) -> int:
@@ -441,12 +472,13 @@ def dcn_core_quantize_fp8(input, rows: int, cols: int, dtype, block_rows: int, q
     rows, cols = int(rows), int(cols)
     kb, mb = _ceil(cols, 128), _ceil(rows, 128)
     whole = block_rows == 128
+    arg = _Args()
     _check(load_library().dcn_core_quantize_fp8(
-        _arg(input, "input", rows * cols, (_torch_dtype(dtype),)), int(dtype), rows, cols,
-        int(block_rows), _arg(q, "q", rows * _ceil(cols, 16) * 16, _CODES),
-        _arg(scales, "scales", kb * (mb if whole else rows), _F32),
-        _arg(q_t, "q_t", cols * _ceil(rows, 16) * 16, _CODES),
-        _arg(scales_t, "scales_t", mb * (kb if whole else cols), _F32), _stream(stream)),
+        arg(input, "input", rows * cols, dtype), dtype, rows, cols, block_rows,
+        arg(q, "q", rows * _ceil(cols, 16) * 16, "codes"),
+        arg(scales, "scales", kb * (mb if whole else rows), DCN_F32),
+        arg(q_t, "q_t", cols * _ceil(rows, 16) * 16, "codes"),
+        arg(scales_t, "scales_t", mb * (kb if whole else cols), DCN_F32), arg.stream(stream)),
         "dcn_core_quantize_fp8")
 
 
@@ -464,14 +496,13 @@ def dcn_core_linear_fp8(input, input_scales, M: int, K: int, weight, weight_scal
         out_dtype = DTYPES[out_dtype]
     M, K, Nout = int(M), int(K), int(Nout)
     kb, pitch = _ceil(K, 128), _ceil(K, 16) * 16
+    arg = _Args()
     _check(load_library().dcn_core_linear_fp8(
-        _arg(input, "input", M * pitch, _CODES),
-        _arg(input_scales, "input_scales", kb * M, _F32), M, K,
-        _arg(weight, "weight", Nout * pitch, _CODES),
-        _arg(weight_scales, "weight_scales", kb * _ceil(Nout, 128), _F32), Nout,
-        _arg(bias, "bias", Nout, _F32),
-        _arg(output, "output", M * Nout, (_torch_dtype(out_dtype),)), int(out_dtype),
-        _workspace_arg(workspace, workspace_bytes), int(workspace_bytes), _stream(stream)),
+        arg(input, "input", M * pitch, "codes"), arg(input_scales, "input_scales", kb * M, DCN_F32),
+        M, K, arg(weight, "weight", Nout * pitch, "codes"),
+        arg(weight_scales, "weight_scales", kb * _ceil(Nout, 128), DCN_F32), Nout,
+        arg(bias, "bias", Nout, DCN_F32), arg(output, "output", M * Nout, out_dtype), out_dtype,
+        arg.workspace(workspace, workspace_bytes), workspace_bytes, arg.stream(stream)),
         "dcn_core_linear_fp8")
 
 
@@ -490,18 +521,18 @@ def dcn_core_linear_fp8_backward(grad_out, dtype, M: int, K: int, Nout: int, wei
     if isinstance(dtype, str):
         dtype = DTYPES[dtype]
     M, K, Nout = int(M), int(K), int(Nout)
-    td = (_torch_dtype(dtype),)
     nb, mb = _ceil(Nout, 128), _ceil(M, 128)
+    arg = _Args()
     _check(load_library().dcn_core_linear_fp8_backward(
-        _arg(grad_out, "grad_out", M * Nout, td), int(dtype), M, K, Nout,
-        _arg(weight_t, "weight_t", K * _ceil(Nout, 16) * 16, _CODES),
-        _arg(weight_t_scales, "weight_t_scales", nb * _ceil(K, 128), _F32),
-        _arg(input_t, "input_t", K * _ceil(M, 16) * 16, _CODES),
-        _arg(input_t_scales, "input_t_scales", mb * K, _F32),
-        _arg(grad_input, "grad_input", M * K, td),
-        _arg(grad_weight, "grad_weight", Nout * K, _F32),
-        _arg(grad_bias, "grad_bias", Nout, _F32), _workspace_arg(workspace, workspace_bytes),
-        int(workspace_bytes), _stream(stream)), "dcn_core_linear_fp8_backward")
+        arg(grad_out, "grad_out", M * Nout, dtype), dtype, M, K, Nout,
+        arg(weight_t, "weight_t", K * _ceil(Nout, 16) * 16, "codes"),
+        arg(weight_t_scales, "weight_t_scales", nb * _ceil(K, 128), DCN_F32),
+        arg(input_t, "input_t", K * _ceil(M, 16) * 16, "codes"),
+        arg(input_t_scales, "input_t_scales", mb * K, DCN_F32),
+        arg(grad_input, "grad_input", M * K, dtype),
+        arg(grad_weight, "grad_weight", Nout * K, DCN_F32),
+        arg(grad_bias, "grad_bias", Nout, DCN_F32), arg.workspace(workspace, workspace_bytes),
+        workspace_bytes, arg.stream(stream)), "dcn_core_linear_fp8_backward")
 
 
 def dcn_core_block_norm(norm: DcnBlockNorm, residual, branch, gate, post_gamma, post_beta,
@@ -510,19 +541,19 @@ def dcn_core_block_norm(norm: DcnBlockNorm, residual, branch, gate, post_gamma, 
     """Post norm, gate, residual scale and the next pre norm in one pass (see
     include/dcn_core.h).  With normed_scales given, normed takes e4m3 codes
     (M, pitch(C)): the input of dcn_core_linear_fp8."""
-    M, C = norm.M, norm.C
-    sd, bd = (_torch_dtype(norm.stream_dtype),), (_torch_dtype(norm.branch_dtype),)
+    M, C, sd, bd = norm.M, norm.C, norm.stream_dtype, norm.branch_dtype
     gates = _ceil(M, norm.rows_per_gate) if norm.rows_per_gate > 0 else 1
     fp8 = normed_scales is not None
+    arg = _Args()
     _check(load_library().dcn_core_block_norm(
-        ctypes.byref(norm), _arg(residual, "residual", M * C, sd), _arg(branch, "branch", M * C, bd),
-        _arg(gate, "gate", gates * C, _F32), _arg(post_gamma, "post_gamma", C, _F32),
-        _arg(post_beta, "post_beta", C, _F32), _arg(pre_gamma, "pre_gamma", C, _F32),
-        _arg(pre_beta, "pre_beta", C, _F32), _arg(residual_out, "residual_out", M * C, sd),
-        _arg(normed, "normed", M * (_ceil(C, 16) * 16 if fp8 else C), _CODES if fp8 else bd),
-        _arg(normed_scales, "normed_scales", _ceil(C, 128) * M, _F32),
-        _arg(post_stats, "post_stats", 2 * M, _F32), _arg(pre_stats, "pre_stats", 2 * M, _F32),
-        _stream(stream)), "dcn_core_block_norm")
+        ctypes.byref(norm), arg(residual, "residual", M * C, sd), arg(branch, "branch", M * C, bd),
+        arg(gate, "gate", gates * C, DCN_F32), arg(post_gamma, "post_gamma", C, DCN_F32),
+        arg(post_beta, "post_beta", C, DCN_F32), arg(pre_gamma, "pre_gamma", C, DCN_F32),
+        arg(pre_beta, "pre_beta", C, DCN_F32), arg(residual_out, "residual_out", M * C, sd),
+        arg(normed, "normed", M * (_ceil(C, 16) * 16 if fp8 else C), "codes" if fp8 else bd),
+        arg(normed_scales, "normed_scales", _ceil(C, 128) * M, DCN_F32),
+        arg(post_stats, "post_stats", 2 * M, DCN_F32), arg(pre_stats, "pre_stats", 2 * M, DCN_F32),
+        arg.stream(stream)), "dcn_core_block_norm")
 
 
 def dcn_core_block_norm_backward_workspace(norm: DcnBlockNorm) -> int:
@@ -537,22 +568,23 @@ def dcn_core_block_norm_backward(norm: DcnBlockNorm, residual_out, branch, gate,
                                  stream=None) -> None:
     """Gradients of dcn_core_block_norm (see include/dcn_core.h); a gradient given
     as None is not computed."""
-    M, C = norm.M, norm.C
-    sd, bd = (_torch_dtype(norm.stream_dtype),), (_torch_dtype(norm.branch_dtype),)
+    M, C, sd, bd = norm.M, norm.C, norm.stream_dtype, norm.branch_dtype
     gates = _ceil(M, norm.rows_per_gate) if norm.rows_per_gate > 0 else 1
-    vec = [_arg(t, n, C, _F32) for t, n in (
-        (grad_post_gamma, "grad_post_gamma"), (grad_post_beta, "grad_post_beta"),
-        (grad_pre_gamma, "grad_pre_gamma"), (grad_pre_beta, "grad_pre_beta"))]
+    arg = _Args()
     _check(load_library().dcn_core_block_norm_backward(
-        ctypes.byref(norm), _arg(residual_out, "residual_out", M * C, sd),
-        _arg(branch, "branch", M * C, bd), _arg(gate, "gate", gates * C, _F32),
-        _arg(post_gamma, "post_gamma", C, _F32), _arg(post_beta, "post_beta", C, _F32),
-        _arg(pre_gamma, "pre_gamma", C, _F32), _arg(post_stats, "post_stats", 2 * M, _F32),
-        _arg(pre_stats, "pre_stats", 2 * M, _F32),
-        _arg(grad_residual_out, "grad_residual_out", M * C, sd),
-        _arg(grad_normed, "grad_normed", M * C, bd), _arg(grad_residual, "grad_residual", M * C, sd),
-        _arg(grad_branch, "grad_branch", M * C, bd), _arg(grad_gate, "grad_gate", gates * C, _F32),
-        *vec, _workspace_arg(workspace, workspace_bytes), int(workspace_bytes), _stream(stream)),
+        ctypes.byref(norm), arg(residual_out, "residual_out", M * C, sd),
+        arg(branch, "branch", M * C, bd), arg(gate, "gate", gates * C, DCN_F32),
+        arg(post_gamma, "post_gamma", C, DCN_F32), arg(post_beta, "post_beta", C, DCN_F32),
+        arg(pre_gamma, "pre_gamma", C, DCN_F32), arg(post_stats, "post_stats", 2 * M, DCN_F32),
+        arg(pre_stats, "pre_stats", 2 * M, DCN_F32),
+        arg(grad_residual_out, "grad_residual_out", M * C, sd),
+        arg(grad_normed, "grad_normed", M * C, bd), arg(grad_residual, "grad_residual", M * C, sd),
+        arg(grad_branch, "grad_branch", M * C, bd), arg(grad_gate, "grad_gate", gates * C, DCN_F32),
+        arg(grad_post_gamma, "grad_post_gamma", C, DCN_F32),
+        arg(grad_post_beta, "grad_post_beta", C, DCN_F32),
+        arg(grad_pre_gamma, "grad_pre_gamma", C, DCN_F32),
+        arg(grad_pre_beta, "grad_pre_beta", C, DCN_F32),
+        arg.workspace(workspace, workspace_bytes), workspace_bytes, arg.stream(stream)),
         "dcn_core_block_norm_backward")
 
 

@@ -48,7 +48,7 @@ auto with_types(const dcn_block_norm* p, F&& f) {
 
 // Calls f(threads a row, vector loads) as constants: the fewest threads that hold
 // `groups` groups of four channels, five each.  Rows that do not start on a vector
-// boundary take single loads and, to save code, one of two mappings.
+// boundary take single loads and, to save code, one of three mappings.
 template <int N>
 struct Int {
   static constexpr int value = N;
@@ -56,7 +56,10 @@ struct Int {
 template <typename F>
 auto with_mapping(int64_t groups, bool vec, F&& f) {
   const int64_t tpr = (groups + kNormGroups - 1) / kNormGroups;
-  if (!vec) return tpr <= 32 ? f(Int<32>(), Int<0>()) : f(Int<256>(), Int<0>());
+  if (!vec) {
+    if (tpr <= 32) return f(Int<32>(), Int<0>());
+    return tpr <= 64 ? f(Int<64>(), Int<0>()) : f(Int<256>(), Int<0>());
+  }
   if (tpr <= 8) return f(Int<8>(), Int<1>());
   if (tpr <= 16) return f(Int<16>(), Int<1>());
   if (tpr <= 32) return f(Int<32>(), Int<1>());
@@ -65,10 +68,26 @@ auto with_mapping(int64_t groups, bool vec, F&& f) {
   return f(Int<256>(), Int<1>());
 }
 
+template <typename Kernel>
+dcn_status launch_backward(Kernel k, size_t smem, const NormBwdArgs& a, int ctas,
+                           cudaStream_t stream) {
+  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) !=
+      cudaSuccess)
+    return DCN_ERR_CUDA;
+  k<<<unsigned(ctas), kNormBwdThreads, smem, stream>>>(a);
+  return launched();
+}
+
 int64_t gates_of(const dcn_block_norm* p, bool gate) {
   return gate && p->rows_per_gate > 0
              ? (int64_t(p->M) + p->rows_per_gate - 1) / p->rows_per_gate
              : 1;
+}
+
+// Vector accesses in the backward: rows of both types start on 16-byte boundaries.
+bool vector_rows(const dcn_block_norm* p) {
+  return (int64_t(p->C) * esize(p->stream_dtype)) % 16 == 0 &&
+         (int64_t(p->C) * esize(p->branch_dtype)) % 16 == 0;
 }
 
 // The backward's split of the rows and its partial sums.
@@ -80,9 +99,12 @@ struct NormSplit {
 NormSplit norm_split(const dcn_block_norm* p, int64_t gates, int sms) {
   NormSplit s;
   const int64_t most = int64_t(sms);
-  // whole steps of the row slots that a CTA has in hand (32 at most)
+  // whole steps of the row slots that a CTA has in hand
+  const int64_t slots = with_mapping((int64_t(p->C) + 3) / 4, vector_rows(p), [](auto tpr, auto) {
+    return kNormThreads / decltype(tpr)::value;
+  });
   int64_t rows = (p->M + most - 1) / most;
-  rows = std::min<int64_t>((rows + 31) / 32 * 32, INT_MAX);
+  rows = std::min<int64_t>((rows + slots - 1) / slots * slots, INT_MAX);
   s.rows_per_cta = int(rows);
   s.ctas = int((p->M + rows - 1) / rows);
   s.s_floats = size_t(s.ctas + gates - 1) * 2 * size_t(p->C);
@@ -242,14 +264,19 @@ dcn_status dcn_core_block_norm_backward(
   a.t_part = t_sums ? ws + split.s_floats : nullptr;
   a.error_word = dev.error_word;
   st = with_types(norm, [&](auto s, auto b) {
-    return with_mapping((int64_t(a.C) + 3) / 4, a.C % 4 == 0, [&](auto tpr, auto vec) {
+    return with_mapping((int64_t(a.C) + 3) / 4, vector_rows(norm), [&](auto tpr, auto v) {
       using TS = decltype(s);
       using TB = decltype(b);
       constexpr int kTpr = decltype(tpr)::value;
-      constexpr bool kVec = decltype(vec)::value != 0;
-      dcn_block_norm_backward_kernel<TS, TB, kTpr, kVec>
-          <<<unsigned(split.ctas), kNormThreads, 0, stream>>>(a);
-      return launched();
+      constexpr bool kVec = decltype(v)::value != 0;
+      if constexpr (kVec) {
+        // the widths of the stages (160, 320, 640, 1280) leave no thread without channels
+        if (a.C == 4 * kNormGroups * kTpr)
+          return launch_backward(dcn_block_norm_backward_kernel<TS, TB, kTpr, true, true>,
+                                 NormBwdShape<TS, TB>::kSmemBytes, a, split.ctas, stream);
+      }
+      return launch_backward(dcn_block_norm_backward_kernel<TS, TB, kTpr, kVec, false>,
+                             NormBwdShape<TS, TB>::kSmemBytes, a, split.ctas, stream);
     });
   });
   if (st != DCN_OK || (!s_sums && !t_sums)) return st;

@@ -12,6 +12,7 @@
 #pragma once
 
 #include "dcn_fp8.cuh"
+#include "dcn_ptx.cuh"
 
 namespace dcn {
 
@@ -325,23 +326,118 @@ struct NormBwdArgs {
   unsigned int* error_word;
 };
 
+// The barrier of the eight working warps (the copying warp has no part in it).
+__device__ __forceinline__ void norm_sync() {
+  asm volatile("bar.sync 9, %0;" ::"n"(kNormThreads) : "memory");
+}
+
+// Untiled copy of whole 16-byte units from global to shared memory.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_addr(dst)),
+      "l"(src), "r"(bytes), "r"(smem_addr(bar))
+      : "memory");
+}
+
+// Channel of value i = 4 j + k of a row's thread t: with VEC groups of four
+// consecutive channels (vector accesses), else every TPR-th channel, so that single
+// accesses of neighbouring threads are neighbours too.
+template <int TPR, bool VEC>
+__device__ __forceinline__ int norm_channel(int t, int j, int k) {
+  return VEC ? 4 * (t + j * TPR) + k : t + (4 * j + k) * TPR;
+}
+
+// Four values of a staged row as two pairs, 0 behind the last channel (FULL: there is
+// none behind it).
+template <typename T, int TPR, bool VEC, bool FULL>
+__device__ __forceinline__ void staged4(const T* row, int t, int j, int C, float2 (&v)[2]) {
+  if constexpr (VEC) {
+    if (FULL || 4 * (t + j * TPR) < C) {
+      if constexpr (sizeof(T) == 4) {
+        const float4 w = *reinterpret_cast<const float4*>(row + 4 * (t + j * TPR));
+        v[0] = make_float2(w.x, w.y);
+        v[1] = make_float2(w.z, w.w);
+      } else {
+        const uint2 w = *reinterpret_cast<const uint2*>(row + 4 * (t + j * TPR));
+        const uint32_t a[2] = {w.x, w.y};
+        v[0] = make_float2(Storage<T>::chan(a, 0), Storage<T>::chan(a, 1));
+        v[1] = make_float2(Storage<T>::chan(a, 2), Storage<T>::chan(a, 3));
+      }
+    } else {
+      v[0] = v[1] = make_float2(0.f, 0.f);
+    }
+  } else {
+    float x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int c = t + (4 * j + k) * TPR;
+      x[k] = c < C ? Storage<T>::to_float(row[c]) : 0.f;
+    }
+    v[0] = make_float2(x[0], x[1]);
+    v[1] = make_float2(x[2], x[3]);
+  }
+}
+
+// The same of an fp32 parameter vector in global memory, `dflt` where there is none.
+template <int TPR, bool VEC, bool FULL>
+__device__ __forceinline__ void param_pairs(const float* p, int t, int j, int C, float dflt,
+                                            float2 (&v)[2]) {
+  if (p == nullptr) {
+    v[0] = v[1] = make_float2(dflt, dflt);
+  } else if constexpr (VEC) {
+    const int c = 4 * (t + j * TPR);
+    const float4 w = FULL || c < C ? __ldg(reinterpret_cast<const float4*>(p + c))
+                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+    v[0] = make_float2(w.x, w.y);
+    v[1] = make_float2(w.z, w.w);
+  } else {
+    float x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int c = t + (4 * j + k) * TPR;
+      x[k] = c < C ? __ldg(p + c) : 0.f;
+    }
+    v[0] = make_float2(x[0], x[1]);
+    v[1] = make_float2(x[2], x[3]);
+  }
+}
+
+template <typename T, int TPR, bool VEC, bool FULL>
+__device__ __forceinline__ void store_pairs(T* row, int t, int j, int C, const float2 (&v)[2]) {
+  const float x[4] = {v[0].x, v[0].y, v[1].x, v[1].y};
+  if constexpr (VEC) {
+    if (FULL || 4 * (t + j * TPR) < C) store4<T, true>(row, 4 * (t + j * TPR), C, x);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int c = t + (4 * j + k) * TPR;
+      if (c < C) Storage<T>::store_float(row + c, x[k]);
+    }
+  }
+}
+
+__device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 neg(float2 v) { return make_float2(-v.x, -v.y); }
+
 // Sum the CTA's row slots' running sums of one array and write them out, fixed order.
-template <int TPR>
-__device__ __forceinline__ void flush_sums(float (&acc)[kNormGroups][4], float* buf, float* out,
+template <int TPR, bool VEC>
+__device__ __forceinline__ void flush_sums(float2 (&acc)[kNormGroups][2], float* buf, float* out,
                                            int C) {
   constexpr int kRows = kNormThreads / TPR;
   constexpr int kCols = 4 * kNormGroups * TPR;  // kRows * kCols = 5120 floats
   const int slot = int(threadIdx.x) / TPR, t = int(threadIdx.x) % TPR;
-  __syncthreads();
+  norm_sync();
 #pragma unroll
   for (int j = 0; j < kNormGroups; ++j) {
-    *reinterpret_cast<float4*>(buf + slot * kCols + 4 * (t + j * TPR)) =
-        make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
+    const float x[4] = {acc[j][0].x, acc[j][0].y, acc[j][1].x, acc[j][1].y};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) acc[j][k] = 0.f;
+    for (int k = 0; k < 4; ++k) buf[slot * kCols + norm_channel<TPR, VEC>(t, j, k)] = x[k];
+    acc[j][0] = acc[j][1] = make_float2(0.f, 0.f);
   }
-  __syncthreads();
-  for (int c = int(threadIdx.x); c < C && c < kCols; c += kNormThreads) {
+  norm_sync();
+  for (int c = int(threadIdx.x); c < C; c += kNormThreads) {
     float s = 0.f;
 #pragma unroll 8
     for (int k = 0; k < kRows; ++k) s += buf[k * kCols + c];
@@ -349,148 +445,289 @@ __device__ __forceinline__ void flush_sums(float (&acc)[kNormGroups][4], float* 
   }
 }
 
-template <typename TS, typename TB, int TPR, bool VEC>
-__global__ void __launch_bounds__(kNormThreads, 1)
+// The rows [base, base + rows) of one step of a CTA: rows of one gate vector, at most
+// as many as it has row slots.
+struct NormSteps {
+  int64_t base, seg_end, end, gate;
+  int per_gate;
+  __device__ __forceinline__ NormSteps(const NormBwdArgs& a) {
+    base = int64_t(blockIdx.x) * a.rows_per_cta;
+    end = min(base + a.rows_per_cta, int64_t(a.M));
+    per_gate = a.rows_per_gate;
+    gate = base / per_gate;
+    seg_end = min(end, (gate + 1) * per_gate);
+  }
+  __device__ __forceinline__ bool valid() const { return base < end; }
+  // Moves on by `rows` row slots; true at the end of a gate vector's rows.
+  __device__ __forceinline__ bool next(int rows) {
+    base += rows;
+    if (base < seg_end) return false;
+    base = seg_end;
+    ++gate;
+    seg_end = min(end, (gate + 1) * per_gate);
+    return true;
+  }
+};
+
+// What a step brings to shared memory: the rows' bytes of up to four tensors, copied
+// as they lie in memory.  A copy starts on a 16-byte boundary at or before the rows;
+// `shift` is where they begin in the buffer.
+struct NormCopy {
+  size_t from;     // first byte copied
+  uint32_t bytes;  // whole 16-byte units copied
+  uint32_t tail;   // bytes behind them, at the tensor's end
+  uint32_t shift;
+};
+
+__device__ __forceinline__ NormCopy norm_copy(int64_t base, int rows, int C, int esize,
+                                              size_t total) {
+  NormCopy c;
+  const size_t first = size_t(base) * C * esize, last = first + size_t(rows) * C * esize;
+  c.from = first & ~size_t(15);
+  const size_t most = total & ~size_t(15);  // nothing behind the tensor is read
+  size_t to = (last + 15) & ~size_t(15);
+  to = to < most ? to : most;
+  c.bytes = uint32_t(to > c.from ? to - c.from : 0);
+  c.tail = uint32_t(last > c.from + c.bytes ? last - c.from - c.bytes : 0);
+  c.shift = uint32_t(first - c.from);
+  return c;
+}
+
+constexpr int kNormBwdThreads = kNormThreads + 32;  // eight working warps and the copying one
+template <typename TS, typename TB>
+struct NormBwdShape {
+  // A step's rows have at most kNormMaxC values; 32 bytes for the shift and the end.
+  static constexpr uint32_t kTileS = kNormMaxC * sizeof(TS) + 32;
+  static constexpr uint32_t kTileB = kNormMaxC * sizeof(TB) + 32;
+  static constexpr uint32_t kStageBytes = 2 * kTileS + 2 * kTileB;
+  static constexpr int kStages = int(180 * 1024 / kStageBytes);  // 2 (fp32) to 4 (2-byte types)
+  static constexpr size_t kSmemBytes = size_t(kStages) * kStageBytes + 128;
+};
+
+// Eight working warps keep the four running sums of their channels in registers (80 a
+// thread) and everything else on chip: a ninth warp copies the steps' rows into a ring
+// in shared memory, so that what is in flight does not depend on registers, and the
+// rows are read from there once for the sums of a row and once for the results.
+template <typename TS, typename TB, int TPR, bool VEC, bool FULL>
+__global__ void __launch_bounds__(kNormBwdThreads, 1)
     dcn_block_norm_backward_kernel(const NormBwdArgs a) {
+  using S = NormBwdShape<TS, TB>;
+  extern __shared__ __align__(128) unsigned char nb_smem[];
   __shared__ float2 s_slots[2 * (kNormThreads / 32)];
   __shared__ __align__(16) float s_buf[kNormMaxC];
+  __shared__ uint64_t full[S::kStages], empty[S::kStages];
+  __shared__ int s_abort;
   constexpr int kRows = kNormThreads / TPR;
+  const int warp = int(threadIdx.x) >> 5, lane = int(threadIdx.x) & 31;
+  volatile int* abort_flag = &s_abort;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S::kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], kNormThreads / 32);
+    }
+    s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+  const size_t total = size_t(a.M) * a.C;
+  // A wait that gives up sets the error word; the roles then run on to their ends
+  // without waiting (the row barriers need every thread).
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (*abort_flag) return false;
+    if (mbar_wait_bounded(bar, parity)) return true;
+    atomicOr(a.error_word, kErrTimeout);
+    *abort_flag = 1;
+    return false;
+  };
+  if (warp == kNormThreads / 32) {
+    // ---- copies ----
+    if (lane == 0) {
+      const char* src[4] = {static_cast<const char*>(a.grad_r), static_cast<const char*>(a.r),
+                            static_cast<const char*>(a.grad_h), static_cast<const char*>(a.branch)};
+      if (a.pre == kNormNone) src[1] = src[2] = nullptr;
+      uint32_t it = 0;
+      for (NormSteps st(a); st.valid(); st.next(kRows), ++it) {
+        const int i = int(it % S::kStages);
+        const uint32_t u = it / S::kStages;
+        if (u > 0 && !wait(&empty[i], (u - 1) & 1)) break;
+        const int rows = int(min(int64_t(kRows), st.seg_end - st.base));
+        const NormCopy cs = norm_copy(st.base, rows, a.C, sizeof(TS), total * sizeof(TS));
+        const NormCopy cb = norm_copy(st.base, rows, a.C, sizeof(TB), total * sizeof(TB));
+        unsigned char* dst = nb_smem + size_t(i) * S::kStageBytes;
+        uint32_t bytes = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const NormCopy& c = k < 2 ? cs : cb;
+          if (src[k] == nullptr) continue;
+          bytes += c.bytes;
+          // the tensor's last bytes, fewer than a unit
+          unsigned char* d = dst + (k < 2 ? k * S::kTileS : 2 * S::kTileS + (k - 2) * S::kTileB);
+          for (uint32_t e = 0; e < c.tail; ++e)
+            d[c.bytes + e] = static_cast<unsigned char>(src[k][c.from + c.bytes + e]);
+        }
+        mbar_arrive_expect_tx(&full[i], bytes);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const NormCopy& c = k < 2 ? cs : cb;
+          if (src[k] == nullptr || c.bytes == 0) continue;
+          unsigned char* d = dst + (k < 2 ? k * S::kTileS : 2 * S::kTileS + (k - 2) * S::kTileB);
+          bulk_load(d, src[k] + c.from, c.bytes, &full[i]);
+        }
+      }
+      // the copies of the last issued stages may still be landing
+      for (uint32_t j = it > uint32_t(S::kStages) ? it - S::kStages : 0; j < it; ++j)
+        (void)mbar_wait_bounded(&full[j % S::kStages], (j / S::kStages) & 1);
+    }
+    return;
+  }
   const int slot = int(threadIdx.x) / TPR, t = int(threadIdx.x) % TPR;
   float2* slots = s_slots + slot * 2 * (TPR / 32);
   int turn = 0;
-  const size_t total = size_t(a.M) * a.C;
-  const int64_t begin = int64_t(blockIdx.x) * a.rows_per_cta;
-  const int64_t end = min(begin + a.rows_per_cta, int64_t(a.M));
   const float inv_c = 1.f / float(a.C);
-
-  float s1[kNormGroups][4], s0[kNormGroups][4], t1[kNormGroups][4], t0[kNormGroups][4];
+  float2 s1[kNormGroups][2], s0[kNormGroups][2], t1[kNormGroups][2], t0[kNormGroups][2];
 #pragma unroll
   for (int j = 0; j < kNormGroups; ++j)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) s1[j][k] = s0[j][k] = t1[j][k] = t0[j][k] = 0.f;
+    for (int k = 0; k < 2; ++k) s1[j][k] = s0[j][k] = t1[j][k] = t0[j][k] = splat(0.f);
 
-  for (int64_t seg = begin; seg < end;) {
-    const int64_t b = seg / a.rows_per_gate;
-    const int64_t seg_end = min(end, (b + 1) * int64_t(a.rows_per_gate));
-    const float* gate = a.gate ? a.gate + size_t(b) * a.C : nullptr;
-    for (int64_t base = seg; base < seg_end; base += kRows) {
-      const bool live = base + slot < seg_end;
-      const int64_t row = live ? base + slot : seg_end - 1;
-      const size_t off = size_t(row) * a.C;
-      float dr[kNormGroups][4], n[kNormGroups][4];
+  uint32_t it = 0;
+  for (NormSteps st(a); st.valid(); ++it) {
+    const int i = int(it % S::kStages);
+    const float* gate = a.gate ? a.gate + size_t(st.gate) * a.C : nullptr;
+    const bool live = st.base + slot < st.seg_end;
+    const int64_t row = live ? st.base + slot : st.seg_end - 1;
+    const int at = int(row - st.base) * a.C;
+    const size_t off = size_t(row) * a.C;
+    const unsigned char* stage = nb_smem + size_t(i) * S::kStageBytes;
+    const uint32_t shift_s = uint32_t(size_t(st.base) * a.C * sizeof(TS)) & 15u;
+    const uint32_t shift_b = uint32_t(size_t(st.base) * a.C * sizeof(TB)) & 15u;
+    const TS* g_r = reinterpret_cast<const TS*>(stage + shift_s) + at;
+    const TS* x_r = reinterpret_cast<const TS*>(stage + S::kTileS + shift_s) + at;
+    const TB* g_h = reinterpret_cast<const TB*>(stage + 2 * S::kTileS + shift_b) + at;
+    const TB* y = reinterpret_cast<const TB*>(stage + 2 * S::kTileS + S::kTileB + shift_b) + at;
+    const bool pre = a.pre != kNormNone, post = a.post != kNormNone;
+    const float m_mean = pre ? __ldg(a.pre_stats + row) : 0.f;
+    const float m_rstd = pre ? __ldg(a.pre_stats + size_t(a.M) + row) : 0.f;
+    const float n_mean = post ? __ldg(a.post_stats + row) : 0.f;
+    const float n_rstd = post ? __ldg(a.post_stats + size_t(a.M) + row) : 1.f;
+    (void)wait(&full[i], (it / S::kStages) & 1);
+
+    float2 dr[kNormGroups][2];
+    if (pre) {
+      const float2 mean2 = splat(-m_mean), rstd2 = splat(m_rstd);
+      float2 sum = splat(0.f), dot = splat(0.f);
 #pragma unroll
       for (int j = 0; j < kNormGroups; ++j) {
-        const int c = 4 * (t + j * TPR);
-        const int w = min(4, a.C - c);
-        const bool in = w <= 0 || in_range_of(a.error_word, off + c, size_t(w), total);
-        if (a.grad_r) {
-          load4<TS, VEC>(static_cast<const TS*>(a.grad_r) + off, in ? c : a.C, a.C, dr[j]);
-        } else {
+        float2 d[2], m[2], gm[2];
+        staged4<TB, TPR, VEC, FULL>(g_h, t, j, a.C, d);
+        staged4<TS, TPR, VEC, FULL>(x_r, t, j, a.C, m);
+        param_pairs<TPR, VEC, FULL>(a.pre_gamma, t, j, a.C, 1.f, gm);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) dr[j][k] = 0.f;
-        }
-      }
-      if (a.pre != kNormNone) {
-        const float mean = a.pre_stats[row], rstd = a.pre_stats[size_t(a.M) + row];
-        float dh[kNormGroups][4];
-        float2 dots = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int j = 0; j < kNormGroups; ++j) {
-          const int c = 4 * (t + j * TPR);
-          const int w = min(4, a.C - c);
-          const bool in = w <= 0 || in_range_of(a.error_word, off + c, size_t(w), total);
-          load4<TB, VEC>(static_cast<const TB*>(a.grad_h) + off, in ? c : a.C, a.C, dh[j]);
-          load4<TS, VEC>(static_cast<const TS*>(a.r) + off, in ? c : a.C, a.C, n[j]);
-          float gm[4];
-          param4<VEC>(a.pre_gamma, c, a.C, 1.f, gm);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            n[j][k] = c + k < a.C ? (n[j][k] - mean) * rstd : 0.f;
-            if (live) {
-              t1[j][k] = fmaf(dh[j][k], n[j][k], t1[j][k]);
-              t0[j][k] += dh[j][k];
-            }
-            dh[j][k] *= gm[k];
-            dots.x += dh[j][k];
-            dots.y = fmaf(dh[j][k], n[j][k], dots.y);
-          }
-        }
-        dots = row_sum2<TPR>(dots, slots, turn);
-        const float d0 = a.pre == kNormLayer ? dots.x * inv_c : 0.f, d1 = dots.y * inv_c;
-#pragma unroll
-        for (int j = 0; j < kNormGroups; ++j)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            dr[j][k] = fmaf(rstd, dh[j][k] - fmaf(n[j][k], d1, d0), dr[j][k]);
-      }
-      if (a.grad_x && live) {
-        TS* o = static_cast<TS*>(a.grad_x) + off;
-#pragma unroll
-        for (int j = 0; j < kNormGroups; ++j) {
-          const int c = 4 * (t + j * TPR);
-          float v[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) v[k] = a.residual_scale * dr[j][k];
-          if (c < a.C && in_range_of(a.error_word, off + c, size_t(min(4, a.C - c)), total))
-            store4<TS, VEC>(o, c, a.C, v);
-        }
-      }
-      if (a.branch == nullptr) continue;
-      const bool norm = a.post != kNormNone;
-      const float mean = norm ? a.post_stats[row] : 0.f;
-      const float rstd = norm ? a.post_stats[size_t(a.M) + row] : 1.f;
-      float2 dots = make_float2(0.f, 0.f);
-#pragma unroll
-      for (int j = 0; j < kNormGroups; ++j) {
-        const int c = 4 * (t + j * TPR);
-        const int w = min(4, a.C - c);
-        const bool in = w <= 0 || in_range_of(a.error_word, off + c, size_t(w), total);
-        load4<TB, VEC>(static_cast<const TB*>(a.branch) + off, in ? c : a.C, a.C, n[j]);
-        float gm[4], gt[4];
-        param4<VEC>(a.post_gamma, c, a.C, 1.f, gm);
-        param4<VEC>(gate, c, a.C, 1.f, gt);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          n[j][k] = c + k < a.C ? (n[j][k] - mean) * rstd : 0.f;
-          if (c + k >= a.C) dr[j][k] = 0.f;
+        for (int k = 0; k < 2; ++k) {
+          m[k] = __fmul2_rn(__fadd2_rn(m[k], mean2), rstd2);  // times d = 0 behind the row
           if (live) {
-            s1[j][k] = fmaf(dr[j][k], n[j][k], s1[j][k]);
-            s0[j][k] += dr[j][k];
+            t1[j][k] = __ffma2_rn(d[k], m[k], t1[j][k]);
+            t0[j][k] = __fadd2_rn(t0[j][k], d[k]);
           }
-          dr[j][k] *= gt[k] * gm[k];
-          dots.x += dr[j][k];
-          dots.y = fmaf(dr[j][k], n[j][k], dots.y);
+          d[k] = __fmul2_rn(d[k], gm[k]);
+          sum = __fadd2_rn(sum, d[k]);
+          dot = __ffma2_rn(d[k], m[k], dot);
         }
       }
-      if (norm) {
-        dots = row_sum2<TPR>(dots, slots, turn);
-        const float d0 = a.post == kNormLayer ? dots.x * inv_c : 0.f, d1 = dots.y * inv_c;
+      const float2 dots =
+          row_sum2<TPR>(make_float2(sum.x + sum.y, dot.x + dot.y), slots, turn);
+      // dr = dr_out + rstd * (d - d0 - m d1), with m = (r - mean) * rstd
+      const float2 d0 = splat(a.pre == kNormLayer ? -dots.x * inv_c : 0.f);
+      const float2 d1 = splat(-dots.y * inv_c);
 #pragma unroll
-        for (int j = 0; j < kNormGroups; ++j)
+      for (int j = 0; j < kNormGroups; ++j) {
+        float2 d[2], m[2], gm[2], g[2];
+        staged4<TB, TPR, VEC, FULL>(g_h, t, j, a.C, d);
+        staged4<TS, TPR, VEC, FULL>(x_r, t, j, a.C, m);
+        param_pairs<TPR, VEC, FULL>(a.pre_gamma, t, j, a.C, 1.f, gm);
+        if (a.grad_r) staged4<TS, TPR, VEC, FULL>(g_r, t, j, a.C, g);
+        else g[0] = g[1] = splat(0.f);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) dr[j][k] = rstd * (dr[j][k] - fmaf(n[j][k], d1, d0));
+        for (int k = 0; k < 2; ++k) {
+          m[k] = __fmul2_rn(__fadd2_rn(m[k], mean2), rstd2);
+          const float2 v = __ffma2_rn(m[k], d1, __ffma2_rn(d[k], gm[k], d0));
+          dr[j][k] = __ffma2_rn(rstd2, v, g[k]);
+        }
       }
-      if (live) {
-        TB* o = static_cast<TB*>(a.grad_y) + off;
+    } else {
+#pragma unroll
+      for (int j = 0; j < kNormGroups; ++j) staged4<TS, TPR, VEC, FULL>(g_r, t, j, a.C, dr[j]);
+    }
+    if (a.grad_x && live) {
+      TS* o = static_cast<TS*>(a.grad_x) + off;
+      const float2 scale = splat(a.residual_scale);
+#pragma unroll
+      for (int j = 0; j < kNormGroups; ++j) {
+        const float2 v[2] = {__fmul2_rn(dr[j][0], scale), __fmul2_rn(dr[j][1], scale)};
+        store_pairs<TS, TPR, VEC, FULL>(o, t, j, a.C, v);
+      }
+    }
+    if (a.branch != nullptr) {
+      const float2 mean2 = splat(-n_mean), rstd2 = splat(n_rstd);
+      float2 sum = splat(0.f), dot = splat(0.f);
+#pragma unroll
+      for (int j = 0; j < kNormGroups; ++j) {
+        float2 n[2], gm[2], gt[2];
+        staged4<TB, TPR, VEC, FULL>(y, t, j, a.C, n);
+        param_pairs<TPR, VEC, FULL>(a.post_gamma, t, j, a.C, 1.f, gm);
+        param_pairs<TPR, VEC, FULL>(gate, t, j, a.C, 1.f, gt);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          n[k] = __fmul2_rn(__fadd2_rn(n[k], mean2), rstd2);
+          if (!FULL) {  // dr behind the row is not 0
+            if (norm_channel<TPR, VEC>(t, j, 2 * k) >= a.C) dr[j][k].x = n[k].x = 0.f;
+            if (norm_channel<TPR, VEC>(t, j, 2 * k + 1) >= a.C) dr[j][k].y = n[k].y = 0.f;
+          }
+          if (live) {
+            s1[j][k] = __ffma2_rn(dr[j][k], n[k], s1[j][k]);
+            s0[j][k] = __fadd2_rn(s0[j][k], dr[j][k]);
+          }
+          dr[j][k] = __fmul2_rn(dr[j][k], __fmul2_rn(gt[k], gm[k]));
+          sum = __fadd2_rn(sum, dr[j][k]);
+          dot = __ffma2_rn(dr[j][k], n[k], dot);
+        }
+      }
+      TB* o = static_cast<TB*>(a.grad_y) + off;
+      if (post) {
+        const float2 dots =
+            row_sum2<TPR>(make_float2(sum.x + sum.y, dot.x + dot.y), slots, turn);
+        const float2 d0 = splat(a.post == kNormLayer ? -dots.x * inv_c : 0.f);
+        const float2 d1 = splat(-dots.y * inv_c);
 #pragma unroll
         for (int j = 0; j < kNormGroups; ++j) {
-          const int c = 4 * (t + j * TPR);
-          if (c < a.C && in_range_of(a.error_word, off + c, size_t(min(4, a.C - c)), total))
-            store4<TB, VEC>(o, c, a.C, dr[j]);
+          float2 n[2];
+          staged4<TB, TPR, VEC, FULL>(y, t, j, a.C, n);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            n[k] = __fmul2_rn(__fadd2_rn(n[k], mean2), rstd2);
+            dr[j][k] = __fmul2_rn(rstd2, __ffma2_rn(n[k], d1, __fadd2_rn(dr[j][k], d0)));
+          }
+          if (live) store_pairs<TB, TPR, VEC, FULL>(o, t, j, a.C, dr[j]);
         }
+      } else if (live) {
+#pragma unroll
+        for (int j = 0; j < kNormGroups; ++j)
+          store_pairs<TB, TPR, VEC, FULL>(o, t, j, a.C, dr[j]);
       }
     }
-    if (a.s_part) {
-      float* o = a.s_part + (size_t(blockIdx.x) + size_t(b)) * 2 * a.C;
-      flush_sums<TPR>(s1, s_buf, o, a.C);
-      flush_sums<TPR>(s0, s_buf, o + a.C, a.C);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[i]);
+    const size_t b = size_t(st.gate);
+    if (st.next(kRows) && a.s_part) {
+      float* o = a.s_part + (size_t(blockIdx.x) + b) * 2 * a.C;
+      flush_sums<TPR, VEC>(s1, s_buf, o, a.C);
+      flush_sums<TPR, VEC>(s0, s_buf, o + a.C, a.C);
     }
-    seg = seg_end;
   }
   if (a.t_part) {
     float* o = a.t_part + size_t(blockIdx.x) * 2 * a.C;
-    flush_sums<TPR>(t1, s_buf, o, a.C);
-    flush_sums<TPR>(t0, s_buf, o + a.C, a.C);
+    flush_sums<TPR, VEC>(t1, s_buf, o, a.C);
+    flush_sums<TPR, VEC>(t0, s_buf, o + a.C, a.C);
   }
 }
 
