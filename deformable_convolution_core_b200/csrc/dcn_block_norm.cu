@@ -179,15 +179,21 @@ dcn_status dcn_core_block_norm(const dcn_block_norm* norm, const void* residual,
       constexpr int kTpr = decltype(tpr)::value;
       constexpr bool kVec = decltype(vec)::value != 0;
       constexpr int kRows = kNormThreads / kTpr;
-      const int64_t grid =
-          std::min<int64_t>((int64_t(a.M) + kRows - 1) / kRows, int64_t(dev.sms) * 8);
-      if (fp8)
-        dcn_block_norm_kernel<TS, TB, kTpr, kVec, true>
-            <<<unsigned(grid), kNormThreads, 0, stream>>>(a);
-      else
-        dcn_block_norm_kernel<TS, TB, kTpr, kVec, false>
-            <<<unsigned(grid), kNormThreads, 0, stream>>>(a);
-      return launched();
+      // every CTA resident, each with rows to load ahead
+      const int64_t grid = std::min<int64_t>((int64_t(a.M) + kRows - 1) / kRows,
+                                             int64_t(dev.sms) * kNormCtas);
+      auto launch = [&](auto k) {
+        k<<<unsigned(grid), kNormThreads, 0, stream>>>(a);
+        return launched();
+      };
+      if constexpr (kVec) {
+        // the widths of the stages (160, 320, 640, 1280) leave no thread without channels
+        if (a.C == 4 * kNormGroups * kTpr)
+          return fp8 ? launch(dcn_block_norm_kernel<TS, TB, kTpr, true, true, true>)
+                     : launch(dcn_block_norm_kernel<TS, TB, kTpr, true, true, false>);
+      }
+      return fp8 ? launch(dcn_block_norm_kernel<TS, TB, kTpr, kVec, false, true>)
+                 : launch(dcn_block_norm_kernel<TS, TB, kTpr, kVec, false, false>);
     });
   });
 }

@@ -11,6 +11,8 @@
 // reduce by shuffles; longer ones add one exchange through shared memory.
 #pragma once
 
+#include <type_traits>
+
 #include "dcn_fp8.cuh"
 #include "dcn_ptx.cuh"
 
@@ -42,32 +44,6 @@ struct NormArgs {
   float* pre_stats;
   unsigned int* error_word;
 };
-
-// Four consecutive channels c .. c + 3 of a row as fp32, 0 behind the last.
-// VEC: rows start on a boundary of four values and C is a multiple of 4.
-// Plain loads: residual_out may be the residual's own buffer.
-template <typename T, bool VEC>
-__device__ __forceinline__ void load4(const T* row, int c, int C, float (&v)[4]) {
-  if constexpr (VEC) {
-    if (c < C) {
-      if constexpr (sizeof(T) == 4) {
-        const float4 w = *reinterpret_cast<const float4*>(row + c);
-        v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
-      } else {
-        const uint2 w = *reinterpret_cast<const uint2*>(row + c);
-        const uint32_t a[2] = {w.x, w.y};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = Storage<T>::chan(a, k);
-      }
-      return;
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = 0.f;
-  } else {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = c + k < C ? Storage<T>::to_float(row[c + k]) : 0.f;
-  }
-}
 
 template <typename T, bool VEC>
 __device__ __forceinline__ void store4(T* row, int c, int C, const float (&v)[4]) {
@@ -137,209 +113,7 @@ __device__ __forceinline__ float row_sum(float v, float2* slots, int& turn) {
   return row_sum2<TPR>(make_float2(v, 0.f), slots, turn).x;
 }
 
-// Mean (0 for RMS) and 1 / sqrt(variance or mean square + eps) of a row's values,
-// which are 0 behind the last channel.  The squares are of centred values: no
-// cancellation, however far the mean is from zero.
-template <int TPR>
-__device__ __forceinline__ float2 row_stats(const float (&v)[kNormGroups][4], int t, int C,
-                                            int kind, float eps, float2* slots, int& turn) {
-  float mean = 0.f;
-  if (kind == kNormLayer) {
-    float s = 0.f;
-#pragma unroll
-    for (int j = 0; j < kNormGroups; ++j) s += (v[j][0] + v[j][1]) + (v[j][2] + v[j][3]);
-    mean = row_sum<TPR>(s, slots, turn) / float(C);
-  }
-  float q = 0.f;
-#pragma unroll
-  for (int j = 0; j < kNormGroups; ++j)
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float d = 4 * (t + j * TPR) + k < C ? v[j][k] - mean : 0.f;
-      q = fmaf(d, d, q);
-    }
-  return make_float2(mean, 1.f / sqrtf(row_sum<TPR>(q, slots, turn) / float(C) + eps));
-}
-
-// TS, TB: storage of the residual stream and of the branch; FP8: normed as e4m3.
-template <typename TS, typename TB, int TPR, bool VEC, bool FP8>
-__global__ void __launch_bounds__(kNormThreads)
-    dcn_block_norm_kernel(const NormArgs a) {
-  __shared__ float2 s_slots[2 * (kNormThreads / 32)];
-  constexpr int kRows = kNormThreads / TPR;  // rows a CTA has in hand
-  const int slot = int(threadIdx.x) / TPR, t = int(threadIdx.x) % TPR;
-  float2* slots = s_slots + slot * 2 * (TPR / 32);
-  int turn = 0;
-  const size_t total = size_t(a.M) * a.C;
-  for (int64_t base = int64_t(blockIdx.x) * kRows; base < a.M;
-       base += int64_t(gridDim.x) * kRows) {
-    // the threads of a warp stay together: a row slot behind the last row works on
-    // the last row and stores nothing
-    const bool live = base + slot < a.M;
-    const int64_t row = live ? base + slot : int64_t(a.M) - 1;
-    const size_t off = size_t(row) * a.C;
-    const TS* x = static_cast<const TS*>(a.residual) + off;
-    const TB* y = static_cast<const TB*>(a.branch) + off;
-    const float* gate =
-        a.gate ? a.gate + size_t(row / a.rows_per_gate) * a.C : nullptr;
-
-    float r[kNormGroups][4], p[kNormGroups][4];
-#pragma unroll
-    for (int j = 0; j < kNormGroups; ++j) {
-      const int c = 4 * (t + j * TPR);
-      const int n = min(4, a.C - c);
-      const bool in = n <= 0 || in_range_of(a.error_word, off + c, size_t(n), total);
-      load4<TS, VEC>(x, in ? c : a.C, a.C, r[j]);
-      if (a.branch) load4<TB, VEC>(y, in ? c : a.C, a.C, p[j]);
-    }
-    if (a.branch) {
-      float2 st = make_float2(0.f, 1.f);
-      if (a.post != kNormNone) {
-        st = row_stats<TPR>(p, t, a.C, a.post, a.post_eps, slots, turn);
-        if (a.post_stats && t == 0 && live) {
-          a.post_stats[row] = st.x;
-          a.post_stats[size_t(a.M) + row] = st.y;
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < kNormGroups; ++j) {
-        const int c = 4 * (t + j * TPR);
-        float gm[4], bt[4], gt[4];
-        param4<VEC>(a.post_gamma, c, a.C, 1.f, gm);
-        param4<VEC>(a.post_beta, c, a.C, 0.f, bt);
-        param4<VEC>(gate, c, a.C, 1.f, gt);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float n = fmaf((p[j][k] - st.x) * st.y, gm[k], bt[k]);
-          r[j][k] = c + k < a.C ? fmaf(gt[k], n, a.residual_scale * r[j][k]) : 0.f;
-        }
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < kNormGroups; ++j)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) r[j][k] *= a.residual_scale;
-    }
-    if (a.residual_out && live) {
-      TS* o = static_cast<TS*>(a.residual_out) + off;
-#pragma unroll
-      for (int j = 0; j < kNormGroups; ++j) {
-        const int c = 4 * (t + j * TPR);
-        if (c < a.C &&
-            in_range_of(a.error_word, off + c, size_t(min(4, a.C - c)), total))
-          store4<TS, VEC>(o, c, a.C, r[j]);
-      }
-    }
-    if (a.pre == kNormNone) continue;
-    const float2 st = row_stats<TPR>(r, t, a.C, a.pre, a.pre_eps, slots, turn);
-    if (a.pre_stats && t == 0 && live) {
-      a.pre_stats[row] = st.x;
-      a.pre_stats[size_t(a.M) + row] = st.y;
-    }
-    if (a.normed == nullptr) continue;
-#pragma unroll
-    for (int j = 0; j < kNormGroups; ++j) {
-      const int c = 4 * (t + j * TPR);
-      float gm[4], bt[4];
-      param4<VEC>(a.pre_gamma, c, a.C, 1.f, gm);
-      param4<VEC>(a.pre_beta, c, a.C, 0.f, bt);
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        r[j][k] = c + k < a.C ? fmaf((r[j][k] - st.x) * st.y, gm[k], bt[k]) : 0.f;
-    }
-    if constexpr (!FP8) {
-      if (live) {
-        TB* o = static_cast<TB*>(a.normed) + off;
-#pragma unroll
-        for (int j = 0; j < kNormGroups; ++j) {
-          const int c = 4 * (t + j * TPR);
-          if (c < a.C &&
-              in_range_of(a.error_word, off + c, size_t(min(4, a.C - c)), total))
-            store4<TB, VEC>(o, c, a.C, r[j]);
-        }
-      }
-    } else {
-      // A block of 128 channels is 32 consecutive groups of four: one j of a whole
-      // warp, or 2 or 4 consecutive j of the row's 16 or 8 threads.
-      constexpr int kSpan = TPR < 32 ? 32 / TPR : 1;
-      uint8_t* codes = static_cast<uint8_t*>(a.normed) + size_t(row) * a.pitch;
-#pragma unroll
-      for (int j0 = 0; j0 < kNormGroups; j0 += kSpan) {
-        float m = 0.f;
-#pragma unroll
-        for (int j = j0; j < j0 + kSpan && j < kNormGroups; ++j)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) m = max_nan(m, fabsf(r[j][k]));
-#pragma unroll
-        for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1)
-          m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-        const BlockScale b = block_scale(m);
-        const int c0 = 4 * (t + j0 * TPR);
-        if (live && c0 < a.C && (t % (TPR < 32 ? TPR : 32)) == 0)
-          a.scales[size_t(c0 / kFp8Block) * a.M + row] = b.scale;
-#pragma unroll
-        for (int j = j0; j < j0 + kSpan && j < kNormGroups; ++j) {
-          const int c = 4 * (t + j * TPR);
-          float q[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) q[k] = c + k < a.C ? __fmul_rn(r[j][k], b.inv) : 0.f;
-          if (live && c < a.pitch &&
-              in_range_of(a.error_word, size_t(row) * a.pitch + c, 4, size_t(a.M) * a.pitch))
-            *reinterpret_cast<uint32_t*>(codes + c) = e4m3x4(q[0], q[1], q[2], q[3]);
-        }
-      }
-    }
-  }
-}
-
-// ---------------------------------------------------------------------------
-// Backward.  With n and m the normalised branch and stream, and back(.) the
-// gradient of a normalisation, dv = rstd * (d - <d> - n <d n>) (no <d> for RMS):
-//   dr = dr_out + back(dh * gq),   dx = a * dr,   dy = back(g * dr * gp),
-// and over the rows, with S1_b = sum dr * n and S0_b = sum dr of gate vector b:
-//   dgq = sum dh * m, dbq = sum dh, dg_b = gp * S1_b + bp * S0_b,
-//   dgp = sum_b g_b * S1_b, dbp = sum_b g_b * S0_b:
-// four running sums a channel give the gradients of five parameter vectors.
-// CTA c takes the rows [c R, (c + 1) R); it writes its S sums whenever the gate
-// vector changes and its dh sums at its end.  The (CTA, gate) pairs that meet form
-// a staircase, so c + b numbers them without a gap or a clash.
-// ---------------------------------------------------------------------------
-struct NormBwdArgs {
-  int M, C;
-  int rows_per_gate, gates;
-  int rows_per_cta;
-  int post, pre;
-  float residual_scale;
-  const void* r;
-  const void* branch;
-  const float* gate;
-  const float* post_gamma;
-  const float* pre_gamma;
-  const float* post_stats;
-  const float* pre_stats;
-  const void* grad_r;
-  const void* grad_h;
-  void* grad_x;
-  void* grad_y;
-  float* s_part;  // (ctas + gates - 1, 2, C): S1, S0 of each meeting pair, or null
-  float* t_part;  // (ctas, 2, C): sums of dh * m and dh, or null
-  unsigned int* error_word;
-};
-
-// The barrier of the eight working warps (the copying warp has no part in it).
-__device__ __forceinline__ void norm_sync() {
-  asm volatile("bar.sync 9, %0;" ::"n"(kNormThreads) : "memory");
-}
-
-// Untiled copy of whole 16-byte units from global to shared memory.
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
-                                          uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          smem_addr(dst)),
-      "l"(src), "r"(bytes), "r"(smem_addr(bar))
-      : "memory");
-}
+__device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
 
 // Channel of value i = 4 j + k of a row's thread t: with VEC groups of four
 // consecutive channels (vector accesses), else every TPR-th channel, so that single
@@ -418,8 +192,319 @@ __device__ __forceinline__ void store_pairs(T* row, int t, int j, int C, const f
   }
 }
 
-__device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
-__device__ __forceinline__ float2 neg(float2 v) { return make_float2(-v.x, -v.y); }
+
+// A thread's values of a row as they lie in memory, loaded a row ahead: vectors of four
+// (VEC; kept packed until the row's turn) or single values.
+template <typename T, int TPR, bool VEC, bool FULL>
+struct RowAhead {
+  using Unit = typename std::conditional<
+      VEC, typename std::conditional<sizeof(T) == 4, float4, uint2>::type, float4>::type;
+  Unit u[kNormGroups];
+  __device__ __forceinline__ void load(const T* row, int t, int C) {
+#pragma unroll
+    for (int j = 0; j < kNormGroups; ++j) {
+      const int c = 4 * (t + j * TPR);
+      if constexpr (VEC) {
+        u[j] = FULL || c < C ? *reinterpret_cast<const Unit*>(row + c) : Unit{};
+      } else {
+        float x[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k] = c + k < C ? Storage<T>::to_float(row[c + k]) : 0.f;
+        u[j] = make_float4(x[0], x[1], x[2], x[3]);
+      }
+    }
+  }
+  __device__ __forceinline__ void widen(int j, float2 (&v)[2]) const {
+    if constexpr (VEC && sizeof(T) == 2) {
+      const uint32_t a[2] = {u[j].x, u[j].y};
+      v[0] = make_float2(Storage<T>::chan(a, 0), Storage<T>::chan(a, 1));
+      v[1] = make_float2(Storage<T>::chan(a, 2), Storage<T>::chan(a, 3));
+    } else {
+      v[0] = make_float2(u[j].x, u[j].y);
+      v[1] = make_float2(u[j].z, u[j].w);
+    }
+  }
+};
+
+// Four values of an fp32 parameter vector of the forward's mapping (groups of four
+// consecutive channels), `dflt` where there is none.
+template <int TPR, bool VEC, bool FULL>
+__device__ __forceinline__ void group_params(const float* p, int t, int j, int C, float dflt,
+                                             float2 (&v)[2]) {
+  if constexpr (VEC) {
+    param_pairs<TPR, true, FULL>(p, t, j, C, dflt, v);
+  } else {
+    float x[4];
+    param4<false>(p, 4 * (t + j * TPR), C, dflt, x);
+    v[0] = make_float2(x[0], x[1]);
+    v[1] = make_float2(x[2], x[3]);
+  }
+}
+
+template <typename T, int TPR, bool VEC, bool FULL>
+__device__ __forceinline__ void store_group(T* row, int t, int j, int C, const float2 (&v)[2]) {
+  const int c = 4 * (t + j * TPR);
+  const float x[4] = {v[0].x, v[0].y, v[1].x, v[1].y};
+  if (FULL || c < C) store4<T, VEC>(row, c, C, x);
+}
+
+// Mean (0 for RMS) and 1 / sqrt(variance or mean square + eps) of a row's values,
+// which are 0 behind the last channel.  The squares are of centred values: no
+// cancellation, however far the mean is from zero.
+template <int TPR, bool FULL>
+__device__ __forceinline__ float2 row_stats(const float2 (&v)[kNormGroups][2], int t, int C,
+                                            float inv_c, int kind, float eps, float2* slots,
+                                            int& turn) {
+  float mean = 0.f;
+  if (kind == kNormLayer) {
+    float2 s = splat(0.f);
+#pragma unroll
+    for (int j = 0; j < kNormGroups; ++j) s = __fadd2_rn(s, __fadd2_rn(v[j][0], v[j][1]));
+    mean = row_sum<TPR>(s.x + s.y, slots, turn) * inv_c;
+  }
+  const float2 m2 = splat(-mean);
+  float2 q = splat(0.f);
+#pragma unroll
+  for (int j = 0; j < kNormGroups; ++j)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float2 d = __fadd2_rn(v[j][k], m2);
+      if (!FULL) {
+        const int c = 4 * (t + j * TPR) + 2 * k;
+        if (c >= C) d.x = 0.f;
+        if (c + 1 >= C) d.y = 0.f;
+      }
+      q = __ffma2_rn(d, d, q);
+    }
+  // rsqrtf is within 2 units in the last place, of 2^-24 relative half steps
+  return make_float2(mean, rsqrtf(fmaf(row_sum<TPR>(q.x + q.y, slots, turn), inv_c, eps)));
+}
+
+// CTAs an SM holds (128 registers a thread).  With the next rows loaded ahead, 16 warps
+// keep about 40 KB in flight, and HBM is at 89% of its copy rate at 589,824 x 160 bf16;
+// three CTAs of 80 registers spill and take 209 us there instead of 132.
+constexpr int kNormCtas = 2;
+
+// TS, TB: storage of the residual stream and of the branch; FULL: every thread has all
+// of its 20 channels (C = 20 TPR); FP8: normed as e4m3.  Each row's values are loaded
+// while the row before is reduced and stored.
+template <typename TS, typename TB, int TPR, bool VEC, bool FULL, bool FP8>
+__global__ void __launch_bounds__(kNormThreads, kNormCtas)
+    dcn_block_norm_kernel(const NormArgs a) {
+  __shared__ float2 s_slots[2 * (kNormThreads / 32)];
+  constexpr int kRows = kNormThreads / TPR;  // rows a CTA has in hand
+  const int slot = int(threadIdx.x) / TPR, t = int(threadIdx.x) % TPR;
+  float2* slots = s_slots + slot * 2 * (TPR / 32);
+  int turn = 0;
+  const float inv_c = 1.f / float(a.C);
+  const size_t total = size_t(a.M) * a.C;
+  const int64_t step = int64_t(gridDim.x) * kRows;
+  RowAhead<TS, TPR, VEC, FULL> xa;
+  RowAhead<TB, TPR, VEC, FULL> ya;
+  auto load = [&](int64_t row) {
+    if (row >= a.M || !in_range_of(a.error_word, size_t(row) * a.C, size_t(a.C), total)) return;
+    xa.load(static_cast<const TS*>(a.residual) + size_t(row) * a.C, t, a.C);
+    if (a.branch) ya.load(static_cast<const TB*>(a.branch) + size_t(row) * a.C, t, a.C);
+  };
+#pragma unroll
+  for (int j = 0; j < kNormGroups; ++j) {
+    xa.u[j] = {};
+    ya.u[j] = {};
+  }
+  const int64_t first = int64_t(blockIdx.x) * kRows;
+  load(first + slot);
+  for (int64_t base = first; base < a.M; base += step) {
+    // the threads of a warp stay together: a row slot behind the last row works on
+    // what it has and stores nothing
+    const bool live = base + slot < a.M;
+    const int row = live ? int(base + slot) : a.M - 1;
+    const size_t off = size_t(row) * a.C;
+    float2 r[kNormGroups][2], p[kNormGroups][2];
+#pragma unroll
+    for (int j = 0; j < kNormGroups; ++j) {
+      xa.widen(j, r[j]);
+      if (a.branch) ya.widen(j, p[j]);
+    }
+    load(base + step + slot);
+    const float2 alpha = splat(a.residual_scale);
+    if (a.branch) {
+      float2 st = make_float2(0.f, 1.f);
+      if (a.post != kNormNone) {
+        st = row_stats<TPR, FULL>(p, t, a.C, inv_c, a.post, a.post_eps, slots, turn);
+        if (a.post_stats && t == 0 && live) {
+          a.post_stats[row] = st.x;
+          a.post_stats[size_t(a.M) + row] = st.y;
+        }
+      }
+      const float* gate = a.gate;
+      if (gate && a.rows_per_gate < a.M) gate += size_t(row / a.rows_per_gate) * a.C;
+      const float2 m2 = splat(-st.x), r2 = splat(st.y);
+#pragma unroll
+      for (int j = 0; j < kNormGroups; ++j) {
+        float2 gt[2];
+        if (a.post != kNormNone) {
+          float2 gm[2], bt[2];
+          group_params<TPR, VEC, FULL>(a.post_gamma, t, j, a.C, 1.f, gm);
+          group_params<TPR, VEC, FULL>(a.post_beta, t, j, a.C, 0.f, bt);
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            p[j][k] = __ffma2_rn(__fmul2_rn(__fadd2_rn(p[j][k], m2), r2), gm[k], bt[k]);
+        }
+        group_params<TPR, VEC, FULL>(gate, t, j, a.C, 1.f, gt);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          r[j][k] = __ffma2_rn(gt[k], p[j][k], __fmul2_rn(alpha, r[j][k]));
+          if (!FULL) {
+            const int c = 4 * (t + j * TPR) + 2 * k;
+            if (c >= a.C) r[j][k].x = 0.f;
+            if (c + 1 >= a.C) r[j][k].y = 0.f;
+          }
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kNormGroups; ++j)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) r[j][k] = __fmul2_rn(alpha, r[j][k]);
+    }
+    if (a.residual_out && live) {
+#pragma unroll
+      for (int j = 0; j < kNormGroups; ++j)
+        store_group<TS, TPR, VEC, FULL>(static_cast<TS*>(a.residual_out) + off, t, j, a.C, r[j]);
+    }
+    if (a.pre == kNormNone) continue;
+    const float2 st = row_stats<TPR, FULL>(r, t, a.C, inv_c, a.pre, a.pre_eps, slots, turn);
+    if (a.pre_stats && t == 0 && live) {
+      a.pre_stats[row] = st.x;
+      a.pre_stats[size_t(a.M) + row] = st.y;
+    }
+    if (a.normed == nullptr) continue;
+    const float2 m2 = splat(-st.x), r2 = splat(st.y);
+#pragma unroll
+    for (int j = 0; j < kNormGroups; ++j) {
+      float2 gm[2], bt[2];
+      group_params<TPR, VEC, FULL>(a.pre_gamma, t, j, a.C, 1.f, gm);
+      group_params<TPR, VEC, FULL>(a.pre_beta, t, j, a.C, 0.f, bt);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        r[j][k] = __ffma2_rn(__fmul2_rn(__fadd2_rn(r[j][k], m2), r2), gm[k], bt[k]);
+        if (!FULL) {
+          const int c = 4 * (t + j * TPR) + 2 * k;
+          if (c >= a.C) r[j][k].x = 0.f;
+          if (c + 1 >= a.C) r[j][k].y = 0.f;
+        }
+      }
+    }
+    if constexpr (!FP8) {
+      if (live) {
+#pragma unroll
+        for (int j = 0; j < kNormGroups; ++j)
+          store_group<TB, TPR, VEC, FULL>(static_cast<TB*>(a.normed) + off, t, j, a.C, r[j]);
+      }
+    } else {
+      // A block of 128 channels is 32 consecutive groups of four: one j of a whole
+      // warp, or 2 or 4 consecutive j of the row's 16 or 8 threads.  Maxima are taken
+      // of the magnitudes' bits, which order as the values do, NaN above all; lane b of
+      // the block's threads then divides for block b, once, and hands inv around.
+      constexpr int kSpan = TPR < 32 ? 32 / TPR : 1;
+      constexpr int kBlocks = (kNormGroups + kSpan - 1) / kSpan;
+      constexpr int kGroup = TPR < 32 ? TPR : 32;  // threads of a block
+      uint32_t top[kBlocks];
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = b * kSpan; j < (b + 1) * kSpan && j < kNormGroups; ++j)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            m = max(m, max(__float_as_uint(fabsf(r[j][k].x)), __float_as_uint(fabsf(r[j][k].y))));
+        if constexpr (kGroup == 32) {
+          m = __reduce_max_sync(0xFFFFFFFFu, m);
+        } else {
+#pragma unroll
+          for (int o = kGroup / 2; o > 0; o >>= 1)
+            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        }
+        top[b] = m;
+      }
+      const int tg = t % kGroup;
+      uint32_t mine = top[0];
+#pragma unroll
+      for (int b = 1; b < kBlocks; ++b) mine = tg == b ? top[b] : mine;
+      const BlockScale scale = block_scale(__uint_as_float(mine));
+      uint8_t* codes = static_cast<uint8_t*>(a.normed) + size_t(row) * a.pitch;
+      // block b of this thread's group starts at channel 4 (t - tg + b kSpan TPR)
+      if (tg < kBlocks) {
+        const int c0 = 4 * (t - tg + tg * kSpan * TPR);
+        if (live && c0 < a.C) a.scales[size_t(c0 / kFp8Block) * a.M + row] = scale.scale;
+      }
+#pragma unroll
+      for (int j = 0; j < kNormGroups; ++j) {
+        const float inv = __shfl_sync(0xFFFFFFFFu, scale.inv, j / kSpan, kGroup);
+        const int c = 4 * (t + j * TPR);
+        float q[4] = {__fmul_rn(r[j][0].x, inv), __fmul_rn(r[j][0].y, inv),
+                      __fmul_rn(r[j][1].x, inv), __fmul_rn(r[j][1].y, inv)};
+        if (!FULL) {  // zeros behind the row, in a block of NaN scale too
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (c + k >= a.C) q[k] = 0.f;
+        }
+        if (live && (FULL || c < a.pitch) &&
+            in_range_of(a.error_word, size_t(row) * a.pitch + c, 4, size_t(a.M) * a.pitch))
+          *reinterpret_cast<uint32_t*>(codes + c) = e4m3x4(q[0], q[1], q[2], q[3]);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Backward.  With n and m the normalised branch and stream, and back(.) the
+// gradient of a normalisation, dv = rstd * (d - <d> - n <d n>) (no <d> for RMS):
+//   dr = dr_out + back(dh * gq),   dx = a * dr,   dy = back(g * dr * gp),
+// and over the rows, with S1_b = sum dr * n and S0_b = sum dr of gate vector b:
+//   dgq = sum dh * m, dbq = sum dh, dg_b = gp * S1_b + bp * S0_b,
+//   dgp = sum_b g_b * S1_b, dbp = sum_b g_b * S0_b:
+// four running sums a channel give the gradients of five parameter vectors.
+// CTA c takes the rows [c R, (c + 1) R); it writes its S sums whenever the gate
+// vector changes and its dh sums at its end.  The (CTA, gate) pairs that meet form
+// a staircase, so c + b numbers them without a gap or a clash.
+// ---------------------------------------------------------------------------
+struct NormBwdArgs {
+  int M, C;
+  int rows_per_gate, gates;
+  int rows_per_cta;
+  int post, pre;
+  float residual_scale;
+  const void* r;
+  const void* branch;
+  const float* gate;
+  const float* post_gamma;
+  const float* pre_gamma;
+  const float* post_stats;
+  const float* pre_stats;
+  const void* grad_r;
+  const void* grad_h;
+  void* grad_x;
+  void* grad_y;
+  float* s_part;  // (ctas + gates - 1, 2, C): S1, S0 of each meeting pair, or null
+  float* t_part;  // (ctas, 2, C): sums of dh * m and dh, or null
+  unsigned int* error_word;
+};
+
+// The barrier of the eight working warps (the copying warp has no part in it).
+__device__ __forceinline__ void norm_sync() {
+  asm volatile("bar.sync 9, %0;" ::"n"(kNormThreads) : "memory");
+}
+
+// Untiled copy of whole 16-byte units from global to shared memory.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_addr(dst)),
+      "l"(src), "r"(bytes), "r"(smem_addr(bar))
+      : "memory");
+}
 
 // Sum the CTA's row slots' running sums of one array and write them out, fixed order.
 template <int TPR, bool VEC>

@@ -30,17 +30,25 @@ dcn_status launched() { return cudaGetLastError() == cudaSuccess ? DCN_OK : DCN_
 // ---------------------------------------------------------------------------
 // Quantiser
 // ---------------------------------------------------------------------------
+template <typename T, bool VEC, bool WHOLE, bool ROWS, bool TRANS>
+void launch_quantize(const QuantArgs& a, unsigned grid, cudaStream_t stream) {
+  if constexpr (!WHOLE) {
+    if (a.col_sums) {
+      dcn_quantize_kernel<T, VEC, false, ROWS, TRANS, true><<<grid, kQuantThreads, 0, stream>>>(a);
+      return;
+    }
+  }
+  if constexpr (ROWS || TRANS)
+    dcn_quantize_kernel<T, VEC, WHOLE, ROWS, TRANS, false><<<grid, kQuantThreads, 0, stream>>>(a);
+}
+
 template <typename T, bool VEC, bool WHOLE>
 void launch_quantize(const QuantArgs& a, unsigned grid, cudaStream_t stream) {
   const bool rows = a.q != nullptr, trans = a.q_t != nullptr;
-  if (rows && trans)
-    dcn_quantize_kernel<T, VEC, WHOLE, true, true><<<grid, kQuantThreads, 0, stream>>>(a);
-  else if (rows)
-    dcn_quantize_kernel<T, VEC, WHOLE, true, false><<<grid, kQuantThreads, 0, stream>>>(a);
-  else if (trans)
-    dcn_quantize_kernel<T, VEC, WHOLE, false, true><<<grid, kQuantThreads, 0, stream>>>(a);
-  else if (!WHOLE)  // column sums alone
-    dcn_quantize_kernel<T, VEC, false, false, false><<<grid, kQuantThreads, 0, stream>>>(a);
+  if (rows && trans) launch_quantize<T, VEC, WHOLE, true, true>(a, grid, stream);
+  else if (rows) launch_quantize<T, VEC, WHOLE, true, false>(a, grid, stream);
+  else if (trans) launch_quantize<T, VEC, WHOLE, false, true>(a, grid, stream);
+  else launch_quantize<T, VEC, WHOLE, false, false>(a, grid, stream);  // column sums alone
 }
 
 dcn_status quantize(const void* x, dcn_dtype dtype, int rows, int cols, int block_rows, void* q,
