@@ -415,22 +415,22 @@ class _Args:
     __slots__ = ("types", "device")
 
     def __init__(self):
-        self.types = _torch_types()
+        self.types = _TORCH or _torch_types()
         self.device = None
 
     def __call__(self, t, name: str, numel: int, kind) -> int | None:
         if t is None or type(t) is int:
             return t
-        dtypes = self.types.get(kind)
         try:
+            if (t.get_device() == self.device and t.numel() == numel
+                    and t.dtype in self.types[kind] and t.is_contiguous()):
+                return t.data_ptr()
             if self.device is None and t.is_cuda:
                 self.device = self.types["device"]()
-            if (t.dtype in dtypes and t.numel() == numel and t.is_cuda
-                    and t.get_device() == self.device and t.is_contiguous()):
-                return t.data_ptr()
-        except (AttributeError, TypeError):
+                return self(t, name, numel, kind)
+        except (AttributeError, TypeError, KeyError):
             pass
-        _bad_arg(t, name, numel, dtypes or ())
+        _bad_arg(t, name, numel, self.types.get(kind, ()))
 
     def workspace(self, t, nbytes: int) -> int | None:
         if t is None or type(t) is int:

@@ -313,6 +313,18 @@ __global__ void __launch_bounds__(kNormThreads, kNormCtas)
   }
   const int64_t first = int64_t(blockIdx.x) * kRows;
   load(first + slot);
+  // The parameters are read between the row's sums, one trip to L2 or HBM after the
+  // other; asked for here, those trips run under the first row's own.
+  if (slot == 0) {
+#pragma unroll
+    for (int j = 0; j < kNormGroups; ++j) {
+      const int c = 4 * (t + j * TPR);
+      if ((c & 31) == 0 && c < a.C) {  // one thread a 128-byte line
+        for (const float* p : {a.post_gamma, a.post_beta, a.pre_gamma, a.pre_beta, a.gate})
+          if (p) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + c));
+      }
+    }
+  }
   for (int64_t base = first; base < a.M; base += step) {
     // the threads of a warp stay together: a row slot behind the last row works on
     // what it has and stores nothing

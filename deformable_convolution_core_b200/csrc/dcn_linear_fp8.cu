@@ -87,6 +87,7 @@ dcn_status quantize(const void* x, dcn_dtype dtype, int rows, int cols, int bloc
 // ---------------------------------------------------------------------------
 constexpr int kRowsKernelMax = 32;  // rows up to which the weight-streaming kernel is used
 constexpr int kMinSplitBlocks = 4;  // K blocks a split has at least
+constexpr int kMaxSplits = 32;
 
 struct LinearPlan {
   bool rows;  // the weight-streaming kernel
@@ -94,23 +95,45 @@ struct LinearPlan {
   int part_pitch;  // row pitch of the partial products (values)
 };
 
+// What an item costs, in cycles: a K block, and the rest of a tile.  Measured at 18944 x
+// 2048 outputs (148 CTAs): K from 2560 to 5120 adds 1170 cycles a block of a 256-column
+// tile and 960 of a 128-column one (its operands are as many bytes for half the work).
+struct TileCost {
+  int bn, block, tile;
+};
+constexpr TileCost kTileCosts[2] = {{256, 1170, 2600}, {128, 960, 1500}};
+constexpr double kJoinBytesPerCycle = 3000.0, kJoinCycles = 6000.0;  // HBM; a second launch
+
+// The column tile and the number of K splits whose rounds of items over the SMs cost
+// least.  Splits pay where there are few tiles and a long inner length (a weight
+// gradient): 2560 x 640 over 36864 takes 60 or 100 tiles of 288 blocks on 148 SMs.
 LinearPlan linear_plan(int M, int K, int N, bool row_scales, int sms) {
   LinearPlan p;
   p.k_blocks = blocks_of(K);
   p.rows = !row_scales && M <= kRowsKernelMax;
   p.m_tiles = blocks_of(M);
-  const int64_t wide = int64_t(p.m_tiles) * ((int64_t(N) + 255) / 256);
-  p.bn = N > 128 && wide >= sms ? 256 : 128;
-  p.n_tiles = int((int64_t(N) + p.bn - 1) / p.bn);
-  p.splits = 1;
-  p.kb_per = p.k_blocks;
   p.part_pitch = int((int64_t(N) + 3) / 4 * 4);
-  const int64_t tiles = int64_t(p.m_tiles) * p.n_tiles;
-  if (!p.rows && tiles < sms) {
-    const int64_t want = std::min<int64_t>(sms / tiles, p.k_blocks / kMinSplitBlocks);
-    if (want > 1) {
-      p.kb_per = int((p.k_blocks + want - 1) / want);
-      p.splits = (p.k_blocks + p.kb_per - 1) / p.kb_per;
+  double best = 0;
+  for (const TileCost& c : kTileCosts) {
+    if (c.bn > 128 && N <= 128) continue;
+    const int64_t n_tiles = (int64_t(N) + c.bn - 1) / c.bn;
+    const int64_t tiles = int64_t(p.m_tiles) * n_tiles;
+    const int most = int(std::min<int64_t>(std::max(1, p.k_blocks / kMinSplitBlocks), kMaxSplits));
+    for (int want = 1; want <= most; ++want) {
+      const int kb_per = (p.k_blocks + want - 1) / want;
+      const int splits = (p.k_blocks + kb_per - 1) / kb_per;
+      const double rounds = double((tiles * splits + sms - 1) / sms);
+      double cost = rounds * (double(kb_per) * c.block + c.tile);
+      if (splits > 1)
+        cost += kJoinCycles + double(splits) * M * double(p.part_pitch) * 8 / kJoinBytesPerCycle;
+      if (best == 0 || cost < best) {
+        best = cost;
+        p.bn = c.bn;
+        p.n_tiles = int(n_tiles);
+        p.splits = splits;
+        p.kb_per = kb_per;
+      }
+      if (tiles * splits >= 4 * int64_t(sms)) break;  // more splits only add to the join
     }
   }
   return p;
@@ -190,8 +213,9 @@ dcn_status linear(const void* a, const float* sa, int M, int K, const void* b, c
     return with_storage(out_dtype, [&](auto tag) {
       using T = decltype(tag);
       const dim3 grid(unsigned((int64_t(N) + 7) / 8));
-      if (M <= 16) dcn_linear_fp8_rows_kernel<T, 1><<<grid, kLrThreads, 0, stream>>>(r);
-      else dcn_linear_fp8_rows_kernel<T, 2><<<grid, kLrThreads, 0, stream>>>(r);
+      if (M <= 8) dcn_linear_fp8_rows_kernel<T, 1, false><<<grid, kLrThreads, 0, stream>>>(r);
+      else if (M <= 16) dcn_linear_fp8_rows_kernel<T, 1, true><<<grid, kLrThreads, 0, stream>>>(r);
+      else dcn_linear_fp8_rows_kernel<T, 2, true><<<grid, kLrThreads, 0, stream>>>(r);
       return launched();
     });
   }

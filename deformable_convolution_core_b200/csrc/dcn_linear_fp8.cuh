@@ -251,8 +251,7 @@ __global__ void __launch_bounds__(kLfThreads, 1)
   uint64_t* empty = full + S::kStages;
   uint64_t* tfull = empty + S::kStages;       // accumulator ready
   uint64_t* tempty = tfull + S::kAccs;    // accumulator read
-  uint64_t* sfull = tempty + S::kAccs;    // scales landed
-  uint64_t* sempty = sfull + kLfScaleSlots;
+  uint64_t* sempty = tempty + S::kAccs;       // scales read
   uint64_t* mma_done = sempty + kLfScaleSlots;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
   int* s_abort = reinterpret_cast<int*>(tmem_slot + 1);
@@ -260,15 +259,14 @@ __global__ void __launch_bounds__(kLfThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], 1 + 32);  // the TMA warp's arrival and the scale warp's copies
       mbar_init(&empty[s], 1);
     }
-    for (int s = 0; s < kLfScaleSlots; ++s) {
-      mbar_init(&sfull[s], 32);
-      mbar_init(&sempty[s], kLfEpiWarps);
-    }
+    for (int s = 0; s < kLfScaleSlots; ++s) mbar_init(&sempty[s], kLfEpiWarps);
     for (int b = 0; b < S::kAccs; ++b) {
-      mbar_init(&tfull[b], 1);
+      // the commit, and an arrival of the issuing thread, which has seen the block's
+      // scales land and so hands them on with the accumulator
+      mbar_init(&tfull[b], 2);
       mbar_init(&tempty[b], kLfEpiWarps);
     }
     mbar_init(mma_done, 1);
@@ -293,8 +291,7 @@ __global__ void __launch_bounds__(kLfThreads, 1)
   };
 
   const uint32_t full_a = smem_addr(full), empty_a = smem_addr(empty), tfull_a = smem_addr(tfull),
-                 tempty_a = smem_addr(tempty), sfull_a = smem_addr(sfull),
-                 sempty_a = smem_addr(sempty);
+                 tempty_a = smem_addr(tempty), sempty_a = smem_addr(sempty);
   // A wait on the phase before a barrier's first succeeds at once: rings start
   // empty, so whoever fills them starts with phase 1 and whoever drains them with 0.
   if (warp == 0) {
@@ -347,6 +344,7 @@ __global__ void __launch_bounds__(kLfThreads, 1)
           if (left > 64) umma_e4m3(d, ad + 4, bd + 4, idesc, 1);
           if (left > 96) umma_e4m3(d, ad + 6, bd + 6, idesc, 1);
           umma_commit_at(tfull_a + 8 * t.slot);
+          mbar_arrive_at(tfull_a + 8 * t.slot);
           umma_commit_at(empty_a + 8 * r.slot);
         }
       }
@@ -357,10 +355,13 @@ __global__ void __launch_bounds__(kLfThreads, 1)
   } else if (warp == 2) {
     // ---- scales ----
     RingPos<kLfScaleSlots> r(1);
+    RingPos<S::kStages> st(1);
     bool stop = false;
     for (LinearItems<BN> w(a); w.valid(a) && !stop; w.next(a)) {
-      for (int kb = w.kb0; kb < w.kb1; ++kb, r.next()) {
-        if (!mbar_wait_watch(sempty_a + 8 * r.slot, r.phase, abort_flag)) {
+      for (int kb = w.kb0; kb < w.kb1; ++kb, r.next(), st.next()) {
+        // a free slot, and the block's stage free too: its barrier's phase is this block's
+        if (!mbar_wait_watch(sempty_a + 8 * r.slot, r.phase, abort_flag) ||
+            !mbar_wait_watch(empty_a + 8 * st.slot, st.phase, abort_flag)) {
           give_up();
           stop = true;
           break;
@@ -380,7 +381,7 @@ __global__ void __launch_bounds__(kLfThreads, 1)
           const int n = w.n0 / kFp8Block + lane;
           cp_async4(slot + kLfBM + lane, n < a.n_blocks ? sb + n : sb, n < a.n_blocks);
         }
-        cp_async_arrive(&sfull[r.slot]);
+        cp_async_arrive(&full[st.slot]);
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -406,14 +407,6 @@ __global__ void __launch_bounds__(kLfThreads, 1)
     fetch_bias();
     RingPos<S::kAccs> t(0);
     RingPos<kLfScaleSlots> sr(0);
-    // The row's scale of a K block (times the block's; column scales stay in the ring).
-    float s_next = 0.f;
-    auto read_scale = [&]() {
-      if (mbar_wait_watch(sfull_a + 8 * sr.slot, sr.phase, abort_flag)) {
-        s_next = row_scale[sr.slot * S::kScaleFloats];
-        if (!ROWB) s_next *= col_scale[sr.slot * S::kScaleFloats];
-      }
-    };
     bool stop = false;
     while (w.valid(a) && !stop) {
       const int col0 = w.n0 + h * kWide;
@@ -439,7 +432,6 @@ __global__ void __launch_bounds__(kLfThreads, 1)
       w.next(a);
       fetch_bias();
       for (int kb = 0; kb < kbs; ++kb, t.next(), sr.next()) {
-        read_scale(); const float2 s2 = make_float2(s_next, s_next);
         const float* s_col = col_scale + sr.slot * S::kScaleFloats;
         const uint32_t s_done = sempty_a + 8 * sr.slot;
         if (!mbar_wait_watch(tfull_a + 8 * t.slot, t.phase, abort_flag)) {
@@ -452,6 +444,9 @@ __global__ void __launch_bounds__(kLfThreads, 1)
         // (columns behind the tensor's last are never stored)
         uint32_t v[2][16];
         tmem_ld16_async(tq + t.slot * BN, v[0]);
+        float s_row = row_scale[sr.slot * S::kScaleFloats];
+        if (!ROWB) s_row *= *s_col;
+        const float2 s2 = make_float2(s_row, s_row);
 #pragma unroll
         for (int c = 0; c < kWide / 16; ++c) {
           tmem_wait16(v[c & 1]);
@@ -609,9 +604,12 @@ __device__ __forceinline__ void load_codes(const uint8_t* row, bool in, int k, i
   }
 }
 
-template <typename T, int MT>  // MT: groups of 16 rows
+// MT: groups of 16 rows; HIGH: there are rows in a group's upper half.  The weights of
+// kAhead K blocks are in flight at a time: a long row is a few round trips to HBM.
+template <typename T, int MT, bool HIGH>
 __global__ void __launch_bounds__(kLrThreads)
     dcn_linear_fp8_rows_kernel(const LinearRowsArgs a) {
+  constexpr int kAhead = MT == 1 ? (HIGH ? 3 : 5) : 2;
   __shared__ float red[kLrWarps][MT * 16][8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
@@ -623,28 +621,43 @@ __global__ void __launch_bounds__(kLrThreads)
   for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int k = 0; k < 4; ++k) acc[i][k] = 0.f;
-#pragma unroll 2
-  for (int kb = warp; kb < a.k_blocks; kb += kLrWarps) {
-    uint32_t wb[8];
-    load_codes(brow, n0 + g < a.N, kb * kFp8Block + 32 * t, a.K, a.pitch, wb);
-    const float sb = __ldg(a.sb + size_t(kb) * a.n_blocks + n0 / kFp8Block);
+  for (int kb0 = warp; kb0 < a.k_blocks; kb0 += kLrWarps * kAhead) {
+    uint32_t wb[kAhead][8], lo[kAhead][MT][8], hi[HIGH ? kAhead : 1][MT][8];
+    float s0[kAhead][MT], s1[kAhead][MT];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      uint32_t lo[8], hi[8];
-      const int m0 = m_base + i * 16 + g, m1 = m0 + 8;
-      load_codes(a.a + size_t(m0) * a.pitch, m0 < a.M, kb * kFp8Block + 32 * t, a.K, a.pitch, lo);
-      load_codes(a.a + size_t(m1) * a.pitch, m1 < a.M, kb * kFp8Block + 32 * t, a.K, a.pitch, hi);
-      const float s0 = m0 < a.M ? sb * __ldg(a.sa + size_t(kb) * a.M + m0) : 0.f;
-      const float s1 = m1 < a.M ? sb * __ldg(a.sa + size_t(kb) * a.M + m1) : 0.f;
-      float d[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int u = 0; u < kAhead; ++u) {
+      const int kb = kb0 + u * kLrWarps, k = kb * kFp8Block + 32 * t;
+      const bool in = kb < a.k_blocks;
+      load_codes(brow, in && n0 + g < a.N, k, a.K, a.pitch, wb[u]);
+      const float sb = in ? __ldg(a.sb + size_t(kb) * a.n_blocks + n0 / kFp8Block) : 0.f;
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        mma_e4m3_16x8x32(d, lo[2 * k], hi[2 * k], lo[2 * k + 1], hi[2 * k + 1], wb[2 * k],
-                         wb[2 * k + 1]);
-      acc[i][0] = fmaf(d[0], s0, acc[i][0]);
-      acc[i][1] = fmaf(d[1], s0, acc[i][1]);
-      acc[i][2] = fmaf(d[2], s1, acc[i][2]);
-      acc[i][3] = fmaf(d[3], s1, acc[i][3]);
+      for (int i = 0; i < MT; ++i) {
+        const int m0 = m_base + i * 16 + g, m1 = m0 + 8;
+        load_codes(a.a + size_t(m0) * a.pitch, in && m0 < a.M, k, a.K, a.pitch, lo[u][i]);
+        s0[u][i] = in && m0 < a.M ? sb * __ldg(a.sa + size_t(kb) * a.M + m0) : 0.f;
+        if constexpr (HIGH) {
+          load_codes(a.a + size_t(m1) * a.pitch, in && m1 < a.M, k, a.K, a.pitch, hi[u][i]);
+          s1[u][i] = in && m1 < a.M ? sb * __ldg(a.sa + size_t(kb) * a.M + m1) : 0.f;
+        } else {
+          s1[u][i] = 0.f;
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      if (kb0 + u * kLrWarps >= a.k_blocks) break;
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_e4m3_16x8x32(d, lo[u][i][2 * k], HIGH ? hi[u][i][2 * k] : 0u, lo[u][i][2 * k + 1],
+                           HIGH ? hi[u][i][2 * k + 1] : 0u, wb[u][2 * k], wb[u][2 * k + 1]);
+        acc[i][0] = fmaf(d[0], s0[u][i], acc[i][0]);
+        acc[i][1] = fmaf(d[1], s0[u][i], acc[i][1]);
+        acc[i][2] = fmaf(d[2], s1[u][i], acc[i][2]);
+        acc[i][3] = fmaf(d[3], s1[u][i], acc[i][3]);
+      }
     }
   }
 #pragma unroll
