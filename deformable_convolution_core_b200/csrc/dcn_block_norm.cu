@@ -93,7 +93,7 @@ bool vector_rows(const dcn_block_norm* p) {
 // The backward's split of the rows and its partial sums.
 struct NormSplit {
   int rows_per_cta, ctas;
-  size_t s_floats, t_floats, gated_floats;
+  size_t s_floats, t_floats;
 };
 
 NormSplit norm_split(const dcn_block_norm* p, int64_t gates, int sms) {
@@ -109,12 +109,11 @@ NormSplit norm_split(const dcn_block_norm* p, int64_t gates, int sms) {
   s.ctas = int((p->M + rows - 1) / rows);
   s.s_floats = size_t(s.ctas + gates - 1) * 2 * size_t(p->C);
   s.t_floats = size_t(s.ctas) * 2 * size_t(p->C);
-  s.gated_floats = gates > 1 ? size_t(gates) * 2 * size_t(p->C) : 0;
   return s;
 }
 
 size_t split_bytes(const NormSplit& s) {
-  return (s.s_floats + s.t_floats + s.gated_floats) * sizeof(float);
+  return (s.s_floats + s.t_floats) * sizeof(float);
 }
 
 }  // namespace
@@ -303,13 +302,7 @@ dcn_status dcn_core_block_norm_backward(
   f.grad_post_beta = grad_post_beta;
   f.grad_pre_gamma = grad_pre_gamma;
   f.grad_pre_beta = grad_pre_beta;
-  const bool join = gates > 1 && (grad_post_gamma || grad_post_beta);
-  f.gated = join ? ws + split.s_floats + split.t_floats : nullptr;
-  const unsigned cols = unsigned((a.C + 31) / 32);
-  dcn_block_norm_sums_kernel<<<dim3(cols, unsigned(std::min<int64_t>(gates + 1, 32768))), 256, 0,
-                               stream>>>(f);
-  if ((st = launched()) != DCN_OK || !join) return st;
-  dcn_block_norm_gated_sum_kernel<<<cols, 256, 0, stream>>>(f);
+  dcn_block_norm_sums_kernel<<<unsigned((a.C + 31) / 32), 32 * kSumGroups, 0, stream>>>(f);
   return launched();
 }
 

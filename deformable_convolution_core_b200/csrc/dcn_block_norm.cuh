@@ -597,14 +597,17 @@ struct NormBwdShape {
   static constexpr uint32_t kTileS = kNormMaxC * sizeof(TS) + 32;
   static constexpr uint32_t kTileB = kNormMaxC * sizeof(TB) + 32;
   static constexpr uint32_t kStageBytes = 2 * kTileS + 2 * kTileB;
-  static constexpr int kStages = int(180 * 1024 / kStageBytes);  // 2 (fp32) to 4 (2-byte types)
-  static constexpr size_t kSmemBytes = size_t(kStages) * kStageBytes + 128;
+  static constexpr int kStages = int(166 * 1024 / kStageBytes);  // 2 (fp32) to 4 (2-byte types)
+  static constexpr uint32_t kParamBytes = 2 * kNormMaxC * 4;     // pre_gamma, gate * post_gamma
+  static constexpr size_t kSmemBytes = size_t(kStages) * kStageBytes + kParamBytes + 128;
 };
 
-// Eight working warps keep the four running sums of their channels in registers (80 a
-// thread) and everything else on chip: a ninth warp copies the steps' rows into a ring
-// in shared memory, so that what is in flight does not depend on registers, and the
-// rows are read from there once for the sums of a row and once for the results.
+// Eight working warps keep the four running sums of their channels (80 registers a
+// thread) and a row's normalised values and gradients (40); a ninth warp copies the
+// steps' rows into a ring in shared memory, so that what is in flight does not depend
+// on registers.  pre_gamma and gate * post_gamma of the rows at hand stand in shared
+// memory too, ones where there are none.  What bounds it is the issue of about 20
+// instructions a value by eight warps.
 template <typename TS, typename TB, int TPR, bool VEC, bool FULL>
 __global__ void __launch_bounds__(kNormBwdThreads, 1)
     dcn_block_norm_backward_kernel(const NormBwdArgs a) {
@@ -681,6 +684,20 @@ __global__ void __launch_bounds__(kNormBwdThreads, 1)
   float2* slots = s_slots + slot * 2 * (TPR / 32);
   int turn = 0;
   const float inv_c = 1.f / float(a.C);
+  float* p_gamma = reinterpret_cast<float*>(nb_smem + size_t(S::kStages) * S::kStageBytes);
+  float* p_weight = p_gamma + kNormMaxC;
+  const bool pre = a.pre != kNormNone, post = a.post != kNormNone;
+  for (int c = int(threadIdx.x); c < a.C; c += kNormThreads)
+    p_gamma[c] = a.pre_gamma ? __ldg(a.pre_gamma + c) : 1.f;
+  auto set_weight = [&](int64_t b) {  // gate b times post_gamma
+    norm_sync();
+    const float* gate = a.gate ? a.gate + size_t(b) * a.C : nullptr;
+    for (int c = int(threadIdx.x); c < a.C; c += kNormThreads)
+      p_weight[c] = (gate ? __ldg(gate + c) : 1.f) * (a.post_gamma ? __ldg(a.post_gamma + c) : 1.f);
+    norm_sync();
+  };
+  // a group of channels behind the row for every thread
+  auto skip = [&](int j) { return !FULL && 4 * j * TPR >= a.C; };
   float2 s1[kNormGroups][2], s0[kNormGroups][2], t1[kNormGroups][2], t0[kNormGroups][2];
 #pragma unroll
   for (int j = 0; j < kNormGroups; ++j)
@@ -688,47 +705,49 @@ __global__ void __launch_bounds__(kNormBwdThreads, 1)
     for (int k = 0; k < 2; ++k) s1[j][k] = s0[j][k] = t1[j][k] = t0[j][k] = splat(0.f);
 
   uint32_t it = 0;
-  for (NormSteps st(a); st.valid(); ++it) {
+  NormSteps st(a);
+  if (st.valid()) set_weight(st.gate);
+  while (st.valid()) {
     const int i = int(it % S::kStages);
-    const float* gate = a.gate ? a.gate + size_t(st.gate) * a.C : nullptr;
     const bool live = st.base + slot < st.seg_end;
     const int64_t row = live ? st.base + slot : st.seg_end - 1;
     const int at = int(row - st.base) * a.C;
     const size_t off = size_t(row) * a.C;
     const unsigned char* stage = nb_smem + size_t(i) * S::kStageBytes;
-    const uint32_t shift_s = uint32_t(size_t(st.base) * a.C * sizeof(TS)) & 15u;
-    const uint32_t shift_b = uint32_t(size_t(st.base) * a.C * sizeof(TB)) & 15u;
+    // vector rows start on 16-byte boundaries
+    const uint32_t shift_s = VEC ? 0u : uint32_t(size_t(st.base) * a.C * sizeof(TS)) & 15u;
+    const uint32_t shift_b = VEC ? 0u : uint32_t(size_t(st.base) * a.C * sizeof(TB)) & 15u;
     const TS* g_r = reinterpret_cast<const TS*>(stage + shift_s) + at;
     const TS* x_r = reinterpret_cast<const TS*>(stage + S::kTileS + shift_s) + at;
     const TB* g_h = reinterpret_cast<const TB*>(stage + 2 * S::kTileS + shift_b) + at;
     const TB* y = reinterpret_cast<const TB*>(stage + 2 * S::kTileS + S::kTileB + shift_b) + at;
-    const bool pre = a.pre != kNormNone, post = a.post != kNormNone;
     const float m_mean = pre ? __ldg(a.pre_stats + row) : 0.f;
     const float m_rstd = pre ? __ldg(a.pre_stats + size_t(a.M) + row) : 0.f;
     const float n_mean = post ? __ldg(a.post_stats + row) : 0.f;
     const float n_rstd = post ? __ldg(a.post_stats + size_t(a.M) + row) : 1.f;
     (void)wait(&full[i], (it / S::kStages) & 1);
 
-    float2 dr[kNormGroups][2];
+    float2 dr[kNormGroups][2], n[kNormGroups][2];  // the gradient; the normalised row
     if (pre) {
       const float2 mean2 = splat(-m_mean), rstd2 = splat(m_rstd);
       float2 sum = splat(0.f), dot = splat(0.f);
 #pragma unroll
       for (int j = 0; j < kNormGroups; ++j) {
-        float2 d[2], m[2], gm[2];
+        if (skip(j)) continue;
+        float2 d[2], gm[2];
         staged4<TB, TPR, VEC, FULL>(g_h, t, j, a.C, d);
-        staged4<TS, TPR, VEC, FULL>(x_r, t, j, a.C, m);
-        param_pairs<TPR, VEC, FULL>(a.pre_gamma, t, j, a.C, 1.f, gm);
+        staged4<TS, TPR, VEC, FULL>(x_r, t, j, a.C, n[j]);
+        staged4<float, TPR, VEC, FULL>(p_gamma, t, j, a.C, gm);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          m[k] = __fmul2_rn(__fadd2_rn(m[k], mean2), rstd2);  // times d = 0 behind the row
+          n[j][k] = __fmul2_rn(__fadd2_rn(n[j][k], mean2), rstd2);  // times d = 0 behind the row
           if (live) {
-            t1[j][k] = __ffma2_rn(d[k], m[k], t1[j][k]);
+            t1[j][k] = __ffma2_rn(d[k], n[j][k], t1[j][k]);
             t0[j][k] = __fadd2_rn(t0[j][k], d[k]);
           }
-          d[k] = __fmul2_rn(d[k], gm[k]);
-          sum = __fadd2_rn(sum, d[k]);
-          dot = __ffma2_rn(d[k], m[k], dot);
+          dr[j][k] = __fmul2_rn(d[k], gm[k]);
+          sum = __fadd2_rn(sum, dr[j][k]);
+          dot = __ffma2_rn(dr[j][k], n[j][k], dot);
         }
       }
       const float2 dots =
@@ -738,28 +757,26 @@ __global__ void __launch_bounds__(kNormBwdThreads, 1)
       const float2 d1 = splat(-dots.y * inv_c);
 #pragma unroll
       for (int j = 0; j < kNormGroups; ++j) {
-        float2 d[2], m[2], gm[2], g[2];
-        staged4<TB, TPR, VEC, FULL>(g_h, t, j, a.C, d);
-        staged4<TS, TPR, VEC, FULL>(x_r, t, j, a.C, m);
-        param_pairs<TPR, VEC, FULL>(a.pre_gamma, t, j, a.C, 1.f, gm);
+        if (skip(j)) continue;
+        float2 g[2] = {splat(0.f), splat(0.f)};
         if (a.grad_r) staged4<TS, TPR, VEC, FULL>(g_r, t, j, a.C, g);
-        else g[0] = g[1] = splat(0.f);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          m[k] = __fmul2_rn(__fadd2_rn(m[k], mean2), rstd2);
-          const float2 v = __ffma2_rn(m[k], d1, __ffma2_rn(d[k], gm[k], d0));
+          const float2 v = __ffma2_rn(n[j][k], d1, __fadd2_rn(dr[j][k], d0));
           dr[j][k] = __ffma2_rn(rstd2, v, g[k]);
         }
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < kNormGroups; ++j) staged4<TS, TPR, VEC, FULL>(g_r, t, j, a.C, dr[j]);
+      for (int j = 0; j < kNormGroups; ++j)
+        if (!skip(j)) staged4<TS, TPR, VEC, FULL>(g_r, t, j, a.C, dr[j]);
     }
     if (a.grad_x && live) {
       TS* o = static_cast<TS*>(a.grad_x) + off;
       const float2 scale = splat(a.residual_scale);
 #pragma unroll
       for (int j = 0; j < kNormGroups; ++j) {
+        if (skip(j)) continue;
         const float2 v[2] = {__fmul2_rn(dr[j][0], scale), __fmul2_rn(dr[j][1], scale)};
         store_pairs<TS, TPR, VEC, FULL>(o, t, j, a.C, v);
       }
@@ -769,26 +786,28 @@ __global__ void __launch_bounds__(kNormBwdThreads, 1)
       float2 sum = splat(0.f), dot = splat(0.f);
 #pragma unroll
       for (int j = 0; j < kNormGroups; ++j) {
-        float2 n[2], gm[2], gt[2];
-        staged4<TB, TPR, VEC, FULL>(y, t, j, a.C, n);
-        param_pairs<TPR, VEC, FULL>(a.post_gamma, t, j, a.C, 1.f, gm);
-        param_pairs<TPR, VEC, FULL>(gate, t, j, a.C, 1.f, gt);
+        if (skip(j)) continue;
+        float2 w[2];
+        staged4<TB, TPR, VEC, FULL>(y, t, j, a.C, n[j]);
+        staged4<float, TPR, VEC, FULL>(p_weight, t, j, a.C, w);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          n[k] = __fmul2_rn(__fadd2_rn(n[k], mean2), rstd2);
-          if (!FULL) {  // dr behind the row is not 0
-            if (norm_channel<TPR, VEC>(t, j, 2 * k) >= a.C) dr[j][k].x = n[k].x = 0.f;
-            if (norm_channel<TPR, VEC>(t, j, 2 * k + 1) >= a.C) dr[j][k].y = n[k].y = 0.f;
+          n[j][k] = __fmul2_rn(__fadd2_rn(n[j][k], mean2), rstd2);
+          if (!FULL) {  // neither is 0 behind the row
+            if (norm_channel<TPR, VEC>(t, j, 2 * k) >= a.C) dr[j][k].x = n[j][k].x = 0.f;
+            if (norm_channel<TPR, VEC>(t, j, 2 * k + 1) >= a.C) dr[j][k].y = n[j][k].y = 0.f;
           }
           if (live) {
-            s1[j][k] = __ffma2_rn(dr[j][k], n[k], s1[j][k]);
+            s1[j][k] = __ffma2_rn(dr[j][k], n[j][k], s1[j][k]);
             s0[j][k] = __fadd2_rn(s0[j][k], dr[j][k]);
           }
-          dr[j][k] = __fmul2_rn(dr[j][k], __fmul2_rn(gt[k], gm[k]));
+          dr[j][k] = __fmul2_rn(dr[j][k], w[k]);
           sum = __fadd2_rn(sum, dr[j][k]);
-          dot = __ffma2_rn(dr[j][k], n[k], dot);
+          dot = __ffma2_rn(dr[j][k], n[j][k], dot);
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[i]);  // the step's rows have all been read
       TB* o = static_cast<TB*>(a.grad_y) + off;
       if (post) {
         const float2 dots =
@@ -796,29 +815,30 @@ __global__ void __launch_bounds__(kNormBwdThreads, 1)
         const float2 d0 = splat(a.post == kNormLayer ? -dots.x * inv_c : 0.f);
         const float2 d1 = splat(-dots.y * inv_c);
 #pragma unroll
-        for (int j = 0; j < kNormGroups; ++j) {
-          float2 n[2];
-          staged4<TB, TPR, VEC, FULL>(y, t, j, a.C, n);
+        for (int j = 0; j < kNormGroups; ++j)
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            n[k] = __fmul2_rn(__fadd2_rn(n[k], mean2), rstd2);
-            dr[j][k] = __fmul2_rn(rstd2, __ffma2_rn(n[k], d1, __fadd2_rn(dr[j][k], d0)));
-          }
-          if (live) store_pairs<TB, TPR, VEC, FULL>(o, t, j, a.C, dr[j]);
-        }
-      } else if (live) {
+          for (int k = 0; k < 2; ++k)
+            if (!skip(j))
+              dr[j][k] = __fmul2_rn(rstd2, __ffma2_rn(n[j][k], d1, __fadd2_rn(dr[j][k], d0)));
+      }
+      if (live) {
 #pragma unroll
         for (int j = 0; j < kNormGroups; ++j)
-          store_pairs<TB, TPR, VEC, FULL>(o, t, j, a.C, dr[j]);
+          if (!skip(j)) store_pairs<TB, TPR, VEC, FULL>(o, t, j, a.C, dr[j]);
       }
+    } else {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[i]);
     }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&empty[i]);
+    ++it;
     const size_t b = size_t(st.gate);
-    if (st.next(kRows) && a.s_part) {
-      float* o = a.s_part + (size_t(blockIdx.x) + b) * 2 * a.C;
-      flush_sums<TPR, VEC>(s1, s_buf, o, a.C);
-      flush_sums<TPR, VEC>(s0, s_buf, o + a.C, a.C);
+    if (st.next(kRows)) {
+      if (a.s_part) {
+        float* o = a.s_part + (size_t(blockIdx.x) + b) * 2 * a.C;
+        flush_sums<TPR, VEC>(s1, s_buf, o, a.C);
+        flush_sums<TPR, VEC>(s0, s_buf, o + a.C, a.C);
+      }
+      if (st.valid() && a.gate) set_weight(st.gate);
     }
   }
   if (a.t_part) {
@@ -841,75 +861,78 @@ struct NormSumArgs {
   float* grad_post_beta;
   float* grad_pre_gamma;
   float* grad_pre_beta;
-  float* gated;  // (gates, 2, C): g_b * S1_b, g_b * S0_b with several gate vectors, else null
 };
 
-// Sums of the pairs (v[i][0][c], v[i][1][c]), i in [first, last), by 8 threads a
-// column in a fixed order; valid in the threads with g = 0.
-__device__ __forceinline__ float2 pair_sum(const float* v, size_t first, size_t last, int C, int c,
-                                           int g, float2 (*s)[33]) {
-  float2 a = make_float2(0.f, 0.f);
-  if (c < C) {
-#pragma unroll 4
-    for (size_t i = first + g; i < last; i += 8) {
-      a.x += v[(2 * i) * C + c];
-      a.y += v[(2 * i + 1) * C + c];
-    }
-  }
-  s[g][threadIdx.x & 31] = a;
+constexpr int kSumGroups = 32;  // warps of a CTA that share 32 columns
+
+// The sum of the warps' values, by warp 0 in the warps' order (valid there).
+__device__ __forceinline__ float2 join_groups(float2 v, int g, float2 (*s)[32]) {
   __syncthreads();
-  if (g == 0)
-#pragma unroll
-    for (int k = 1; k < 8; ++k) {
-      a.x += s[k][threadIdx.x & 31].x;
-      a.y += s[k][threadIdx.x & 31].y;
-    }
-  return a;
-}
-
-// blockIdx.y < gates: the S sums of one gate vector; blockIdx.y = gates: the dh sums.
-__global__ void __launch_bounds__(256) dcn_block_norm_sums_kernel(const NormSumArgs a) {
-  __shared__ float2 s[8][33];
-  const int c = int(blockIdx.x) * 32 + int(threadIdx.x & 31), g = int(threadIdx.x >> 5);
-  const bool writes = g == 0 && c < a.C;
-  for (int64_t b = blockIdx.y; b <= a.gates; b += gridDim.y) {
-    __syncthreads();
-    if (b == a.gates) {
-      if (a.t_part == nullptr) continue;
-      const float2 v = pair_sum(a.t_part, 0, size_t(a.ctas), a.C, c, g, s);
-      if (writes && a.grad_pre_gamma) a.grad_pre_gamma[c] = v.x;
-      if (writes && a.grad_pre_beta) a.grad_pre_beta[c] = v.y;
-      continue;
-    }
-    if (a.s_part == nullptr) continue;
-    const int64_t r0 = b * a.rows_per_gate;
-    const int64_t r1 = min(r0 + a.rows_per_gate, int64_t(a.M));
-    const size_t first = size_t(r0 / a.rows_per_cta) + size_t(b);
-    const size_t last = size_t((r1 - 1) / a.rows_per_cta) + size_t(b) + 1;
-    const float2 v = pair_sum(a.s_part, first, last, a.C, c, g, s);
-    if (!writes) continue;
-    const float gp = a.post_gamma ? a.post_gamma[c] : 1.f;
-    const float bp = a.post_beta ? a.post_beta[c] : 0.f;
-    const float gt = a.gate ? a.gate[size_t(b) * a.C + c] : 1.f;
-    if (a.grad_gate) a.grad_gate[size_t(b) * a.C + c] = fmaf(gp, v.x, bp * v.y);
-    if (a.gated) {
-      a.gated[size_t(2 * b) * a.C + c] = gt * v.x;
-      a.gated[size_t(2 * b + 1) * a.C + c] = gt * v.y;
-    } else {
-      if (a.grad_post_gamma) a.grad_post_gamma[c] = gt * v.x;
-      if (a.grad_post_beta) a.grad_post_beta[c] = gt * v.y;
+  s[g][threadIdx.x & 31] = v;
+  __syncthreads();
+  if (g == 0) {
+#pragma unroll 8
+    for (int k = 1; k < kSumGroups; ++k) {
+      v.x += s[k][threadIdx.x & 31].x;
+      v.y += s[k][threadIdx.x & 31].y;
     }
   }
+  return v;
 }
 
-// The post norm's parameters over several gate vectors.
-__global__ void __launch_bounds__(256) dcn_block_norm_gated_sum_kernel(const NormSumArgs a) {
-  __shared__ float2 s[8][33];
+// The CTAs' partial sums to the parameters' gradients: 32 columns a CTA, a lane a
+// column.  Many gate vectors are dealt out to the 32 warps; the partial sums of few, and
+// those of dh, are.
+__global__ void __launch_bounds__(32 * kSumGroups)
+    dcn_block_norm_sums_kernel(const NormSumArgs a) {
+  __shared__ float2 s[kSumGroups][32];
   const int c = int(blockIdx.x) * 32 + int(threadIdx.x & 31), g = int(threadIdx.x >> 5);
-  const float2 v = pair_sum(a.gated, 0, size_t(a.gates), a.C, c, g, s);
-  if (g == 0 && c < a.C) {
-    if (a.grad_post_gamma) a.grad_post_gamma[c] = v.x;
-    if (a.grad_post_beta) a.grad_post_beta[c] = v.y;
+  const bool in = c < a.C;
+  auto add = [&](const float* v, size_t i, float2& to) {
+    to.x += v[(2 * i) * a.C + c];
+    to.y += v[(2 * i + 1) * a.C + c];
+  };
+  if (a.s_part) {
+    const float gp = in && a.post_gamma ? a.post_gamma[c] : 1.f;
+    const float bp = in && a.post_beta ? a.post_beta[c] : 0.f;
+    float2 gated = make_float2(0.f, 0.f);
+    // the gradient of gate b, and its part of the post norm's parameters
+    auto finish = [&](int64_t b, float2 v) {
+      const float gt = a.gate ? a.gate[size_t(b) * a.C + c] : 1.f;
+      if (a.grad_gate) a.grad_gate[size_t(b) * a.C + c] = fmaf(gp, v.x, bp * v.y);
+      gated.x = fmaf(gt, v.x, gated.x);
+      gated.y = fmaf(gt, v.y, gated.y);
+    };
+    const bool deal = a.gates >= kSumGroups;
+    for (int64_t b = deal ? g : 0; b < a.gates; b += deal ? kSumGroups : 1) {
+      const int64_t r0 = b * a.rows_per_gate;
+      const int64_t r1 = min(r0 + a.rows_per_gate, int64_t(a.M));
+      const size_t first = size_t(r0 / a.rows_per_cta) + size_t(b);
+      const size_t last = size_t((r1 - 1) / a.rows_per_cta) + size_t(b) + 1;
+      float2 v = make_float2(0.f, 0.f);
+      if (in)
+#pragma unroll 4
+        for (size_t i = first + (deal ? 0 : g); i < last; i += deal ? 1 : kSumGroups)
+          add(a.s_part, i, v);
+      if (!deal) v = join_groups(v, g, s);
+      if (in && (deal || g == 0)) finish(b, v);
+    }
+    if (deal) gated = join_groups(gated, g, s);
+    if (in && g == 0) {
+      if (a.grad_post_gamma) a.grad_post_gamma[c] = gated.x;
+      if (a.grad_post_beta) a.grad_post_beta[c] = gated.y;
+    }
+  }
+  if (a.t_part) {
+    float2 v = make_float2(0.f, 0.f);
+    if (in)
+#pragma unroll 4
+      for (int i = g; i < a.ctas; i += kSumGroups) add(a.t_part, size_t(i), v);
+    v = join_groups(v, g, s);
+    if (in && g == 0) {
+      if (a.grad_pre_gamma) a.grad_pre_gamma[c] = v.x;
+      if (a.grad_pre_beta) a.grad_pre_beta[c] = v.y;
+    }
   }
 }
 
