@@ -11,9 +11,11 @@
 // Kernel: persistent CTAs over (128-row, BN-column, K split) items, columns
 // fastest (the row tile of A stays in L2 while B's column tiles pass).  Warp 0
 // streams 128-byte K blocks of A and B into a shared-memory ring by TMA (128-byte
-// swizzle); one thread of warp 1 issues tcgen05.mma (kind::f8f6f4, K = 32) for one
-// block at a time into one of 512 / BN accumulators; warp 2 brings the blocks' scales
-// into a ring of their own with asynchronous copies; sixteen epilogue warps
+// swizzle); one thread each of warps 1 and 3 issues tcgen05.mma (kind::f8f6f4, K = 32)
+// for every other block, into every other one of 512 / BN accumulators (issuing a
+// block's four MMAs takes as long as they run, about 550 cycles, and the waits before
+// them another 350, which the other thread's MMAs now fill); warp 2 brings the blocks'
+// scales into a ring of their own with asynchronous copies; sixteen epilogue warps
 // (four lane quarters x four column quarters) read each accumulator back, scale and
 // add it, and at an item's end store it by TMA from a swizzled 4 KB buffer each.  The
 // sums of a 128 x 256 tile take 64 of the 96 registers of every epilogue thread, and
@@ -33,7 +35,7 @@ namespace dcn {
 
 constexpr int kLfBM = 128;
 constexpr int kLfBK = 128;  // values and bytes of a K block: one scale, one swizzle atom
-constexpr int kLfFrontWarps = 4;  // TMA, MMA, scales, none
+constexpr int kLfFrontWarps = 4;  // TMA, MMA, scales, MMA
 constexpr int kLfEpiWarps = 16;
 constexpr int kLfThreads = (kLfFrontWarps + kLfEpiWarps) * 32;
 constexpr uint32_t kLfTmemCols = 512;
@@ -253,7 +255,7 @@ __global__ void __launch_bounds__(kLfThreads, 1)
   uint64_t* tempty = tfull + S::kAccs;    // accumulator read
   uint64_t* sempty = tempty + S::kAccs;       // scales read
   uint64_t* mma_done = sempty + kLfScaleSlots;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 2);
   int* s_abort = reinterpret_cast<int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -269,7 +271,8 @@ __global__ void __launch_bounds__(kLfThreads, 1)
       mbar_init(&tfull[b], 2);
       mbar_init(&tempty[b], kLfEpiWarps);
     }
-    mbar_init(mma_done, 1);
+    mbar_init(&mma_done[0], 1);
+    mbar_init(&mma_done[1], 1);
     *s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -316,17 +319,18 @@ __global__ void __launch_bounds__(kLfThreads, 1)
       for (uint32_t j = issued > uint32_t(S::kStages) ? issued - S::kStages : 0; j < issued; ++j)
         (void)mbar_wait_bounded(&full[j % S::kStages], (j / S::kStages) & 1);
     }
-  } else if (warp == 1) {
-    // ---- MMA issuer: one K block, one accumulator ----
+  } else if (warp == 1 || warp == 3) {
+    // ---- MMA issuers: every other K block, one accumulator a block ----
     if (lane == 0) {
       RingPos<S::kStages> r(0);
       RingPos<S::kAccs> t(1);
       const uint64_t a_desc0 = umma_desc_sw128(smem_addr(stage_a));
       const uint64_t b_desc0 = umma_desc_sw128(smem_addr(stage_b));
-      bool stop = false;
+      bool mine = warp == 1, stop = false;
       for (LinearItems<BN> w(a); w.valid(a) && !stop; w.next(a)) {
         const uint32_t idesc = umma_idesc_e4m3_f32(kLfBM, min(BN, (a.N - w.n0 + 15) / 16 * 16));
-        for (int kb = w.kb0; kb < w.kb1; ++kb, r.next(), t.next()) {
+        for (int kb = w.kb0; kb < w.kb1; ++kb, r.next(), t.next(), mine = !mine) {
+          if (!mine) continue;
           if (!mbar_wait_watch(full_a + 8 * r.slot, r.phase, abort_flag) ||
               !mbar_wait_watch(tempty_a + 8 * t.slot, t.phase, abort_flag)) {
             give_up();
@@ -348,9 +352,9 @@ __global__ void __launch_bounds__(kLfThreads, 1)
           umma_commit_at(empty_a + 8 * r.slot);
         }
       }
-      // every MMA issued has retired before the accumulators are freed
-      umma_commit(mma_done);
-      (void)mbar_wait_bounded(mma_done, 0);
+      // every MMA this thread issued has retired before the accumulators are freed
+      umma_commit(&mma_done[warp >> 1]);
+      (void)mbar_wait_bounded(&mma_done[warp >> 1], 0);
     }
   } else if (warp == 2) {
     // ---- scales ----
