@@ -659,6 +659,11 @@ __global__ void __launch_bounds__(kNormBwdThreads, 1)
         for (int k = 0; k < 4; ++k) {
           const NormCopy& c = k < 2 ? cs : cb;
           if (src[k] == nullptr) continue;
+          if (!in_range_of(a.error_word, c.from, size_t(c.bytes) + c.tail,
+                           total * (k < 2 ? sizeof(TS) : sizeof(TB)))) {
+            src[k] = nullptr;  // the bounds-checked build: no copies of it from here on
+            continue;
+          }
           bytes += c.bytes;
           // the tensor's last bytes, fewer than a unit
           unsigned char* d = dst + (k < 2 ? k * S::kTileS : 2 * S::kTileS + (k - 2) * S::kTileB);

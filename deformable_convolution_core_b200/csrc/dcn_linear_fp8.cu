@@ -23,6 +23,10 @@ int blocks_of(int n) { return int((int64_t(n) + kFp8Block - 1) / kFp8Block); }
 int64_t pitch_of(int cols) { return (int64_t(cols) + 15) / 16 * 16; }
 size_t round16(size_t n) { return (n + 15) / 16 * 16; }
 
+// Extents up to here: an index may run a tile, or a few K blocks of the row kernel's
+// look-ahead, behind the last row or column without leaving 31 bits.
+constexpr int kMaxExtent = INT_MAX - 65535;
+
 bool valid_dtype(dcn_dtype d) { return d == DCN_F32 || d == DCN_BF16 || d == DCN_F16; }
 
 dcn_status launched() { return cudaGetLastError() == cudaSuccess ? DCN_OK : DCN_ERR_CUDA; }
@@ -58,7 +62,6 @@ dcn_status quantize(const void* x, dcn_dtype dtype, int rows, int cols, int bloc
   a.x = x;
   a.rows = rows;
   a.cols = cols;
-  if (pitch_of(cols) > INT_MAX || pitch_of(rows) > INT_MAX) return DCN_ERR_UNSUPPORTED;
   a.pitch = int(pitch_of(cols));
   a.pitch_t = int(pitch_of(rows));
   a.col_tiles = blocks_of(cols);
@@ -143,6 +146,14 @@ size_t plan_workspace(const LinearPlan& p, int M) {
   return p.splits > 1 ? size_t(p.splits) * size_t(M) * size_t(p.part_pitch) * sizeof(float) : 0;
 }
 
+// Whether a plan's kernel can run: known before anything is enqueued.
+bool plan_runs(const LinearPlan& p, const DeviceInfo& dev) {
+  return p.rows ||
+         (tensor_map_encoder() != nullptr &&
+          size_t(dev.smem_optin) >= std::max(LfShape<128>::kSmemBytes, LfShape<256>::kSmemBytes) &&
+          int64_t(p.m_tiles) * p.n_tiles * p.splits <= kMaxExtent);
+}
+
 // 2-D map of e4m3 codes (inner: values of a row) with a (128, rows) box, 128-byte swizzle.
 dcn_status codes_map(CUtensorMap* map, const void* base, int inner, int64_t pitch, int outer,
                      int rows) {
@@ -199,7 +210,6 @@ dcn_status linear(const void* a, const float* sa, int M, int K, const void* b, c
                   cudaStream_t stream) {
   const LinearPlan p = linear_plan(M, K, N, row_scales, dev.sms);
   const int64_t pitch = pitch_of(K);
-  if (pitch > INT_MAX) return DCN_ERR_UNSUPPORTED;
   if (p.rows) {
     LinearRowsArgs r;
     r.M = M; r.N = N; r.K = K;
@@ -221,11 +231,8 @@ dcn_status linear(const void* a, const float* sa, int M, int K, const void* b, c
   }
   const size_t need = plan_workspace(p, M);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return DCN_ERR_INVALID_ARG;
-  if (tensor_map_encoder() == nullptr) return DCN_ERR_UNSUPPORTED;
-  if (size_t(dev.smem_optin) < std::max(LfShape<128>::kSmemBytes, LfShape<256>::kSmemBytes))
-    return DCN_ERR_UNSUPPORTED;
+  if (!plan_runs(p, dev)) return DCN_ERR_UNSUPPORTED;
   const int64_t items = int64_t(p.m_tiles) * p.n_tiles * p.splits;
-  if (items > INT_MAX) return DCN_ERR_UNSUPPORTED;
   const bool split = p.splits > 1;
   const dcn_dtype kernel_dtype = split ? DCN_F32 : out_dtype;
   LinearArgs g;
@@ -268,6 +275,9 @@ dcn_status linear(const void* a, const float* sa, int M, int K, const void* b, c
 }
 
 bool valid_sizes(int M, int K, int N) { return M >= 1 && K >= 1 && N >= 1; }
+bool supported_sizes(int M, int K, int N) {
+  return M <= kMaxExtent && K <= kMaxExtent && N <= kMaxExtent;
+}
 
 // Workspace of the backward, in order (each part 16-byte aligned).
 struct BackwardLayout {
@@ -311,6 +321,7 @@ dcn_status dcn_core_quantize_fp8(const void* input, dcn_dtype dtype, int rows, i
   if ((q == nullptr) != (scales == nullptr) || (q_t == nullptr) != (scales_t == nullptr) ||
       (!q && !q_t))
     return DCN_ERR_INVALID_ARG;
+  if (rows > kMaxExtent || cols > kMaxExtent) return DCN_ERR_UNSUPPORTED;
   if (!aligned(input, 16) || !aligned(q, 16) || !aligned(q_t, 16) || !aligned(scales, 4) ||
       !aligned(scales_t, 4))
     return DCN_ERR_UNSUPPORTED;
@@ -322,7 +333,8 @@ dcn_status dcn_core_quantize_fp8(const void* input, dcn_dtype dtype, int rows, i
 
 size_t dcn_core_linear_fp8_workspace(int M, int K, int Nout) {
   DeviceInfo dev;
-  if (!valid_sizes(M, K, Nout) || device_info(&dev) != DCN_OK) return 0;
+  if (!valid_sizes(M, K, Nout) || !supported_sizes(M, K, Nout) || device_info(&dev) != DCN_OK)
+    return 0;
   return plan_workspace(linear_plan(M, K, Nout, false, dev.sms), M);
 }
 
@@ -333,6 +345,7 @@ dcn_status dcn_core_linear_fp8(const void* input, const float* input_scales, int
   if (!input || !input_scales || !weight || !weight_scales || !output ||
       !valid_sizes(M, K, Nout) || !valid_dtype(out_dtype))
     return DCN_ERR_INVALID_ARG;
+  if (!supported_sizes(M, K, Nout)) return DCN_ERR_UNSUPPORTED;
   if (!aligned(input, 16) || !aligned(weight, 16) || !aligned(output, 16) ||
       !aligned(workspace, 16) || !aligned(input_scales, 4) || !aligned(weight_scales, 4) ||
       !aligned(bias, 4))
@@ -345,7 +358,8 @@ dcn_status dcn_core_linear_fp8(const void* input, const float* input_scales, int
 
 size_t dcn_core_linear_fp8_backward_workspace(int M, int K, int Nout) {
   DeviceInfo dev;
-  if (!valid_sizes(M, K, Nout) || device_info(&dev) != DCN_OK) return 0;
+  if (!valid_sizes(M, K, Nout) || !supported_sizes(M, K, Nout) || device_info(&dev) != DCN_OK)
+    return 0;
   return backward_layout(M, K, Nout, dev.sms).bytes;
 }
 
@@ -360,6 +374,7 @@ dcn_status dcn_core_linear_fp8_backward(const void* grad_out, dcn_dtype dtype, i
   if (!grad_input && !grad_weight && !grad_bias) return DCN_ERR_INVALID_ARG;
   if (grad_input && (!weight_t || !weight_t_scales)) return DCN_ERR_INVALID_ARG;
   if (grad_weight && (!input_t || !input_t_scales)) return DCN_ERR_INVALID_ARG;
+  if (!supported_sizes(M, K, Nout)) return DCN_ERR_UNSUPPORTED;
   if (!aligned(grad_out, 16) || !aligned(weight_t, 16) || !aligned(input_t, 16) ||
       !aligned(grad_input, 16) || !aligned(grad_weight, 16) || !aligned(workspace, 16) ||
       !aligned(weight_t_scales, 4) || !aligned(input_t_scales, 4) || !aligned(grad_bias, 4))
@@ -368,6 +383,10 @@ dcn_status dcn_core_linear_fp8_backward(const void* grad_out, dcn_dtype dtype, i
   if (device_info(&dev) != DCN_OK) return DCN_ERR_CUDA;
   const BackwardLayout l = backward_layout(M, K, Nout, dev.sms);
   if (workspace_bytes < l.bytes) return DCN_ERR_INVALID_ARG;
+  if ((grad_input && !plan_runs(linear_plan(M, Nout, K, false, dev.sms), dev)) ||
+      (grad_weight && !plan_runs(linear_plan(Nout, M, K, true, dev.sms), dev)) ||
+      int64_t(blocks_of(M)) * blocks_of(Nout) > INT_MAX)
+    return DCN_ERR_UNSUPPORTED;
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   float* scales = reinterpret_cast<float*>(ws + l.scales);
   float* scales_t = reinterpret_cast<float*>(ws + l.scales_t);

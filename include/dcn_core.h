@@ -389,7 +389,8 @@ DCN_API dcn_status dcn_core_linear_bf16(const void* input, int M, int K, const v
  * even).  448 is the largest e4m3 value; the floor keeps an all-zero block (scale
  * 2^-64) and inv finite.  A block that holds a NaN or an infinity gets the scale
  * NaN and NaN codes, so that whatever it takes part in becomes NaN.
- * Sizes are 64-bit products: a matrix may hold 2^31 values and more.
+ * Sizes are 64-bit products: a matrix may hold 2^31 values and more.  Each extent is at
+ * most 2^31 - 65536 (else DCN_ERR_UNSUPPORTED).
  * ------------------------------------------------------------------------- */
 
 /* Row pitch in bytes of an e4m3 matrix with `cols` columns (0 for cols < 1). */
@@ -457,7 +458,9 @@ DCN_API size_t dcn_core_linear_fp8_backward_workspace(int M, int K, int Nout);
  *   grad_input (M, K) of dtype; grad_weight fp32 (Nout, K); grad_bias fp32 (Nout);
  *             each may be NULL and is then not computed (one at least is given;
  *             weight_t may be NULL without grad_input, input_t without grad_weight)
- * Matrices and workspace 16-byte aligned; errors as for dcn_core_linear_fp8.
+ * Matrices and workspace 16-byte aligned; errors as for dcn_core_linear_fp8, except
+ * that a launch that fails part-way (DCN_ERR_CUDA) may leave the steps before it
+ * enqueued.
  */
 DCN_API dcn_status dcn_core_linear_fp8_backward(
     const void* grad_out, dcn_dtype dtype, int M, int K, int Nout, const void* weight_t,

@@ -65,6 +65,7 @@ QUANT = dict(input=FAKE, rows=4, cols=40, dtype="bf16", block_rows=1, q=FAKE, sc
     (dict(block_rows=0), INVALID), (dict(q=None), INVALID), (dict(scales=None), INVALID),
     (dict(q_t=None), INVALID), (dict(scales_t=None), INVALID),
     (dict(q=None, scales=None, q_t=None, scales_t=None), INVALID),
+    (dict(rows=2**31 - 1), UNSUPPORTED), (dict(cols=2**31 - 65535), UNSUPPORTED),
     (dict(input=FAKE + 8), UNSUPPORTED), (dict(q=FAKE + 1), UNSUPPORTED),
     (dict(q_t=FAKE + 4), UNSUPPORTED), (dict(scales=FAKE + 2), UNSUPPORTED),
 ])
@@ -80,6 +81,8 @@ LINEAR = dict(input=FAKE, input_scales=FAKE, M=200, K=64, weight=FAKE, weight_sc
     (dict(input=None), INVALID), (dict(input_scales=None), INVALID), (dict(weight=None), INVALID),
     (dict(weight_scales=None), INVALID), (dict(output=None), INVALID), (dict(M=0), INVALID),
     (dict(K=0), INVALID), (dict(Nout=-1), INVALID), (dict(out_dtype=9), INVALID),
+    (dict(M=2**31 - 1), UNSUPPORTED), (dict(K=2**31 - 1), UNSUPPORTED),
+    (dict(Nout=2**31 - 65535), UNSUPPORTED),
     (dict(input=FAKE + 4), UNSUPPORTED), (dict(weight=FAKE + 8), UNSUPPORTED),
     (dict(output=FAKE + 2), UNSUPPORTED), (dict(bias=FAKE + 2), UNSUPPORTED),
     (dict(workspace=FAKE + 4), UNSUPPORTED), (dict(input_scales=FAKE + 1), UNSUPPORTED),
@@ -99,6 +102,7 @@ BACK = dict(grad_out=FAKE, dtype="bf16", M=200, K=64, Nout=32, weight_t=FAKE, we
     (dict(weight_t_scales=None), INVALID), (dict(input_t=None), INVALID),
     (dict(input_t_scales=None), INVALID), (dict(workspace=None), INVALID),
     (dict(grad_input=None, grad_weight=None, grad_bias=None), INVALID),
+    (dict(M=2**31 - 1), UNSUPPORTED), (dict(K=2**31 - 1), UNSUPPORTED),
     (dict(grad_out=FAKE + 8), UNSUPPORTED), (dict(grad_weight=FAKE + 4), UNSUPPORTED),
     (dict(workspace=FAKE + 8), UNSUPPORTED), (dict(grad_bias=FAKE + 2), UNSUPPORTED),
 ])
