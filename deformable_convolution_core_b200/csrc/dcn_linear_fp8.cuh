@@ -47,6 +47,9 @@ template <int BN>
 struct LfShape {
   static constexpr int kStages = BN == 256 ? 3 : 4;
   static constexpr int kAccs = int(kLfTmemCols) / BN;
+  // The MMA threads' order of waits needs an accumulator's last block to be no older
+  // than a stage's, or both rings to be dealt out evenly to the two threads.
+  static_assert(kAccs % 2 == 0 && (kAccs <= kStages || kStages % 2 == 0), "rings of the MMA threads");
   static constexpr uint32_t kStageBytes = uint32_t(kLfBM + BN) * kLfBK;
   static constexpr int kScaleFloats = kLfBM + BN;  // a slot: row scales, column scales
   static constexpr size_t kSmemBytes = 1024 /* alignment slack */ + size_t(kStages) * kStageBytes +
@@ -331,8 +334,12 @@ __global__ void __launch_bounds__(kLfThreads, 1)
         const uint32_t idesc = umma_idesc_e4m3_f32(kLfBM, min(BN, (a.N - w.n0 + 15) / 16 * 16));
         for (int kb = w.kb0; kb < w.kb1; ++kb, r.next(), t.next(), mine = !mine) {
           if (!mine) continue;
-          if (!mbar_wait_watch(full_a + 8 * r.slot, r.phase, abort_flag) ||
-              !mbar_wait_watch(tempty_a + 8 * t.slot, t.phase, abort_flag)) {
+          // The accumulator first: once the epilogue, which takes the blocks in order, has
+          // read this thread's last one, the block that had this block's stage before,
+          // the other thread's perhaps, has long been multiplied.  So the stage's barrier
+          // is at this block's phase, and the parity of an older one cannot be taken for it.
+          if (!mbar_wait_watch(tempty_a + 8 * t.slot, t.phase, abort_flag) ||
+              !mbar_wait_watch(full_a + 8 * r.slot, r.phase, abort_flag)) {
             give_up();
             stop = true;
             break;
