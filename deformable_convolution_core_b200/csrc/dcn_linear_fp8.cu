@@ -88,7 +88,7 @@ dcn_status quantize(const void* x, dcn_dtype dtype, int rows, int cols, int bloc
 // ---------------------------------------------------------------------------
 // Matrix product
 // ---------------------------------------------------------------------------
-constexpr int kRowsKernelMax = 32;  // rows up to which the weight-streaming kernel is used
+constexpr int kRowsKernelMax = 8;   // rows up to which the weight-streaming kernel is used
 constexpr int kMinSplitBlocks = 4;  // K blocks a split has at least
 constexpr int kMaxSplits = 32;
 
@@ -99,12 +99,12 @@ struct LinearPlan {
 };
 
 // What an item costs, in cycles: a K block, and the rest of a tile.  Measured at 18944 x
-// 2048 outputs (148 CTAs): K from 2560 to 5120 adds 1170 cycles a block of a 256-column
-// tile and 960 of a 128-column one (its operands are as many bytes for half the work).
+// 2048 outputs (148 CTAs): K from 2560 to 5120 adds 1100 cycles a block of a 256-column
+// tile and 720 of a 128-column one.
 struct TileCost {
   int bn, block, tile;
 };
-constexpr TileCost kTileCosts[2] = {{256, 1170, 2600}, {128, 960, 1500}};
+constexpr TileCost kTileCosts[2] = {{256, 1100, 2600}, {128, 720, 1500}};
 constexpr double kJoinBytesPerCycle = 3000.0, kJoinCycles = 6000.0;  // HBM; a second launch
 
 // The column tile and the number of K splits whose rounds of items over the SMs cost
@@ -216,16 +216,17 @@ dcn_status linear(const void* a, const float* sa, int M, int K, const void* b, c
     r.k_blocks = p.k_blocks;
     r.pitch = int(pitch);
     r.n_blocks = blocks_of(N);
+    r.wk = 1;  // so many warps a column group that each has one round of blocks
+    while (r.wk < kLrWarps && r.wk * kLrAhead < r.k_blocks) r.wk *= 2;
     r.a = static_cast<const uint8_t*>(a);
     r.b = static_cast<const uint8_t*>(b);
     r.sa = sa; r.sb = sb; r.bias = bias; r.out = out;
     r.error_word = dev.error_word;
     return with_storage(out_dtype, [&](auto tag) {
       using T = decltype(tag);
-      const dim3 grid(unsigned((int64_t(N) + 7) / 8));
-      if (M <= 8) dcn_linear_fp8_rows_kernel<T, 1, false><<<grid, kLrThreads, 0, stream>>>(r);
-      else if (M <= 16) dcn_linear_fp8_rows_kernel<T, 1, true><<<grid, kLrThreads, 0, stream>>>(r);
-      else dcn_linear_fp8_rows_kernel<T, 2, true><<<grid, kLrThreads, 0, stream>>>(r);
+      const int64_t columns = kLrWarps / r.wk * 8;
+      const unsigned grid = unsigned((int64_t(N) + columns - 1) / columns);
+      dcn_linear_fp8_rows_kernel<T><<<grid, kLrThreads, 0, stream>>>(r);
       return launched();
     });
   }

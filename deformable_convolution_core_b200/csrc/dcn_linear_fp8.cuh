@@ -565,16 +565,19 @@ __global__ void __launch_bounds__(256)
 }
 
 // ---------------------------------------------------------------------------
-// Few rows.  The weight is read once and nothing else matters, so the work is
-// spread over many small CTAs instead of 128-row tiles: a CTA owns 8 output
-// columns, its 8 warps take the K blocks in turn, and mma.sync m16n8k32 multiplies
-// 16 rows by the 8 columns (rows that are not there cost no memory traffic).  A
-// lane reads 32 contiguous bytes of its weight row a block, two 16-byte loads; the
-// order of the 128 products is permuted the same way in both operands, so no
-// shuffle is needed.  The warps' sums are joined in shared memory in a fixed order.
-// ---------------------------------------------------------------------------
+// Few rows.  The weight is read once and nothing else matters, so the work is spread
+// over many warps instead of 128-row tiles: a warp owns 8 output columns and every
+// `wk`-th K block, five blocks in flight at a time, and mma.sync m16n8k32 multiplies the
+// rows (its first eight) by the 8 columns (rows that are not there cost no traffic).  A lane
+// reads 32 contiguous bytes of its weight row a block, two 16-byte loads; the order of
+// the 128 products is permuted the same way in both operands, so no shuffle is needed.
+// The `wk` warps of a column group are joined in shared memory in a fixed order.  Bound
+// by latency: 1 to 8 rows of 5120 x 1280 take 5.3 to 5.5 us from launch to launch (the
+// tile kernel 8.6, the weight's 6.6 MB alone 1.0), of 1280 x 5120 5.5 to 5.8 (7.7).  With
+// rows in the MMA's upper half too, 9 to 16 took 10 to 11: the tile kernel has those.
 struct LinearRowsArgs {
   int M, N, K, k_blocks, pitch, n_blocks;
+  int wk;  // warps that share a column group: a power of two up to kLrWarps
   const uint8_t* a;
   const uint8_t* b;
   const float* sa;
@@ -586,6 +589,7 @@ struct LinearRowsArgs {
 
 constexpr int kLrWarps = 8;
 constexpr int kLrThreads = kLrWarps * 32;
+constexpr int kLrAhead = 5;  // K blocks in flight a warp
 
 __device__ __forceinline__ void mma_e4m3_16x8x32(float (&d)[4], uint32_t a0, uint32_t a1,
                                                  uint32_t a2, uint32_t a3, uint32_t b0,
@@ -615,75 +619,49 @@ __device__ __forceinline__ void load_codes(const uint8_t* row, bool in, int k, i
   }
 }
 
-// MT: groups of 16 rows; HIGH: there are rows in a group's upper half.  The weights of
-// kAhead K blocks are in flight at a time: a long row is a few round trips to HBM.
-template <typename T, int MT, bool HIGH>
+template <typename T>
 __global__ void __launch_bounds__(kLrThreads)
     dcn_linear_fp8_rows_kernel(const LinearRowsArgs a) {
-  constexpr int kAhead = MT == 1 ? (HIGH ? 3 : 5) : 2;
-  __shared__ float red[kLrWarps][MT * 16][8];
+  __shared__ float red[kLrWarps][8][8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const int n0 = int(blockIdx.x) * 8;
-  const int m_base = int(blockIdx.y) * MT * 16;
+  const int groups = kLrWarps / a.wk;  // column groups of the CTA
+  const int n_cta = int(blockIdx.x) * groups * 8;
+  const int n0 = n_cta + warp / a.wk * 8;
+  const bool col = n0 + g < a.N;
   const uint8_t* brow = a.b + size_t(min(n0 + g, a.N - 1)) * a.pitch;
-  float acc[MT][4];
+  float acc[2] = {0.f, 0.f};  // row g, columns 2 t and 2 t + 1
+  for (int kb0 = warp & (a.wk - 1); kb0 < a.k_blocks; kb0 += a.wk * kLrAhead) {
+    uint32_t wb[kLrAhead][8], wa[kLrAhead][8];
+    float s[kLrAhead];
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int k = 0; k < 4; ++k) acc[i][k] = 0.f;
-  for (int kb0 = warp; kb0 < a.k_blocks; kb0 += kLrWarps * kAhead) {
-    uint32_t wb[kAhead][8], lo[kAhead][MT][8], hi[HIGH ? kAhead : 1][MT][8];
-    float s0[kAhead][MT], s1[kAhead][MT];
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int kb = kb0 + u * kLrWarps, k = kb * kFp8Block + 32 * t;
-      const bool in = kb < a.k_blocks;
-      load_codes(brow, in && n0 + g < a.N, k, a.K, a.pitch, wb[u]);
+    for (int u = 0; u < kLrAhead; ++u) {
+      const int kb = kb0 + u * a.wk, k = kb * kFp8Block + 32 * t;
+      const bool in = kb < a.k_blocks && n0 < a.N;
+      load_codes(brow, in && col, k, a.K, a.pitch, wb[u]);
+      load_codes(a.a + size_t(g) * a.pitch, in && g < a.M, k, a.K, a.pitch, wa[u]);
       const float sb = in ? __ldg(a.sb + size_t(kb) * a.n_blocks + n0 / kFp8Block) : 0.f;
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        const int m0 = m_base + i * 16 + g, m1 = m0 + 8;
-        load_codes(a.a + size_t(m0) * a.pitch, in && m0 < a.M, k, a.K, a.pitch, lo[u][i]);
-        s0[u][i] = in && m0 < a.M ? sb * __ldg(a.sa + size_t(kb) * a.M + m0) : 0.f;
-        if constexpr (HIGH) {
-          load_codes(a.a + size_t(m1) * a.pitch, in && m1 < a.M, k, a.K, a.pitch, hi[u][i]);
-          s1[u][i] = in && m1 < a.M ? sb * __ldg(a.sa + size_t(kb) * a.M + m1) : 0.f;
-        } else {
-          s1[u][i] = 0.f;
-        }
-      }
+      s[u] = in && g < a.M ? sb * __ldg(a.sa + size_t(kb) * a.M + g) : 0.f;
     }
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      if (kb0 + u * kLrWarps >= a.k_blocks) break;
+    for (int u = 0; u < kLrAhead; ++u) {
+      if (kb0 + u * a.wk >= a.k_blocks) break;
+      float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        float d[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_e4m3_16x8x32(d, lo[u][i][2 * k], HIGH ? hi[u][i][2 * k] : 0u, lo[u][i][2 * k + 1],
-                           HIGH ? hi[u][i][2 * k + 1] : 0u, wb[u][2 * k], wb[u][2 * k + 1]);
-        acc[i][0] = fmaf(d[0], s0[u][i], acc[i][0]);
-        acc[i][1] = fmaf(d[1], s0[u][i], acc[i][1]);
-        acc[i][2] = fmaf(d[2], s1[u][i], acc[i][2]);
-        acc[i][3] = fmaf(d[3], s1[u][i], acc[i][3]);
-      }
+      for (int k = 0; k < 4; ++k)
+        mma_e4m3_16x8x32(d, wa[u][2 * k], 0u, wa[u][2 * k + 1], 0u, wb[u][2 * k], wb[u][2 * k + 1]);
+      acc[0] = fmaf(d[0], s[u], acc[0]);
+      acc[1] = fmaf(d[1], s[u], acc[1]);
     }
   }
-#pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    *reinterpret_cast<float2*>(&red[warp][i * 16 + g][2 * t]) = make_float2(acc[i][0], acc[i][1]);
-    *reinterpret_cast<float2*>(&red[warp][i * 16 + g + 8][2 * t]) =
-        make_float2(acc[i][2], acc[i][3]);
-  }
+  *reinterpret_cast<float2*>(&red[warp][g][2 * t]) = make_float2(acc[0], acc[1]);
   __syncthreads();
-  for (int e = int(threadIdx.x); e < MT * 128; e += kLrThreads) {
-    const int m = m_base + (e >> 3), n = n0 + (e & 7);
+  for (int e = int(threadIdx.x); e < groups * 64; e += kLrThreads) {
+    const int m = (e >> 3) & 7, c = e & 7, grp = e >> 6;
+    const int n = n_cta + grp * 8 + c;
     if (m >= a.M || n >= a.N) continue;
-    float v = red[0][e >> 3][e & 7];
-#pragma unroll
-    for (int w = 1; w < kLrWarps; ++w) v += red[w][e >> 3][e & 7];
+    float v = red[grp * a.wk][m][c];
+    for (int w = 1; w < a.wk; ++w) v += red[grp * a.wk + w][m][c];
     if (a.bias) v += __ldg(a.bias + n);
     const size_t o = size_t(m) * a.N + n;
     if (in_range_of(a.error_word, o, 1, size_t(a.M) * a.N))

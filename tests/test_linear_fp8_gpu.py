@@ -47,7 +47,8 @@ def forward(a, sa, w, sw, M, K, N, bias, out_dtype, stream=None):
 
 
 SIZES = [  # rows, inner, columns
-    (1, 16, 8), (1, 1, 1), (1, 160, 640), (3, 37, 5), (16, 128, 128), (17, 300, 200), (31, 5120, 130),
+    (1, 16, 8), (1, 1, 1), (1, 160, 640), (3, 37, 5), (8, 5120, 75), (8, 1300, 1000), (7, 20000, 24), (9, 64, 40),
+    (16, 128, 128), (17, 300, 200), (31, 5120, 130),
     (32, 640, 160), (33, 16, 8), (40, 1, 1), (64, 31, 17), (100, 5120, 200), (128, 128, 128),
     (129, 160, 640), (200, 336, 450), (300, 1280, 333), (1000, 640, 161), (2000, 200, 257),
     (19000, 136, 200), (19100, 129, 391)]
