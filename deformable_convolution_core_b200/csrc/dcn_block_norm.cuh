@@ -887,7 +887,7 @@ __device__ __forceinline__ float2 join_groups(float2 v, int g, float2 (*s)[32]) 
 
 // The CTAs' partial sums to the parameters' gradients: 32 columns a CTA, a lane a
 // column.  Many gate vectors are dealt out to the 32 warps; the partial sums of few, and
-// those of dh, are.
+// those of dh (blockIdx.y = 1), are.
 __global__ void __launch_bounds__(32 * kSumGroups)
     dcn_block_norm_sums_kernel(const NormSumArgs a) {
   __shared__ float2 s[kSumGroups][32];
@@ -897,7 +897,7 @@ __global__ void __launch_bounds__(32 * kSumGroups)
     to.x += v[(2 * i) * a.C + c];
     to.y += v[(2 * i + 1) * a.C + c];
   };
-  if (a.s_part) {
+  if (a.s_part && blockIdx.y == 0) {
     const float gp = in && a.post_gamma ? a.post_gamma[c] : 1.f;
     const float bp = in && a.post_beta ? a.post_beta[c] : 0.f;
     float2 gated = make_float2(0.f, 0.f);
@@ -910,10 +910,11 @@ __global__ void __launch_bounds__(32 * kSumGroups)
     };
     const bool deal = a.gates >= kSumGroups;
     for (int64_t b = deal ? g : 0; b < a.gates; b += deal ? kSumGroups : 1) {
-      const int64_t r0 = b * a.rows_per_gate;
-      const int64_t r1 = min(r0 + a.rows_per_gate, int64_t(a.M));
-      const size_t first = size_t(r0 / a.rows_per_cta) + size_t(b);
-      const size_t last = size_t((r1 - 1) / a.rows_per_cta) + size_t(b) + 1;
+      // rows fit 31 bits: 32-bit divisions
+      const uint32_t r0 = uint32_t(b * a.rows_per_gate);
+      const uint32_t r1 = uint32_t(min((b + 1) * a.rows_per_gate, int64_t(a.M)));
+      const size_t first = size_t(r0 / uint32_t(a.rows_per_cta)) + size_t(b);
+      const size_t last = size_t((r1 - 1) / uint32_t(a.rows_per_cta)) + size_t(b) + 1;
       float2 v = make_float2(0.f, 0.f);
       if (in)
 #pragma unroll 4
@@ -928,7 +929,7 @@ __global__ void __launch_bounds__(32 * kSumGroups)
       if (a.grad_post_beta) a.grad_post_beta[c] = gated.y;
     }
   }
-  if (a.t_part) {
+  if (a.t_part && blockIdx.y == 1) {
     float2 v = make_float2(0.f, 0.f);
     if (in)
 #pragma unroll 4

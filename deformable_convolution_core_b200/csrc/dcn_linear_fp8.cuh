@@ -472,13 +472,19 @@ __global__ void __launch_bounds__(kLfThreads, 1)
             }
           }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            float2 sc = s2;
-            if constexpr (ROWB)
-              sc = __fmul2_rn(s2, *reinterpret_cast<const float2*>(s_col + c * 16 + 2 * i));
-            acc[c * 8 + i] = __ffma2_rn(make_float2(__uint_as_float(v[c & 1][2 * i]),
-                                                    __uint_as_float(v[c & 1][2 * i + 1])),
-                                        sc, acc[c * 8 + i]);
+          for (int i = 0; i < 8; i += 2) {
+            float2 sc[2] = {s2, s2};
+            if constexpr (ROWB) {  // the same four columns' scales for every lane: one read
+              const float4 cs = *reinterpret_cast<const float4*>(s_col + c * 16 + 2 * i);
+              sc[0] = __fmul2_rn(s2, make_float2(cs.x, cs.y));
+              sc[1] = __fmul2_rn(s2, make_float2(cs.z, cs.w));
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              acc[c * 8 + i + k] =
+                  __ffma2_rn(make_float2(__uint_as_float(v[c & 1][2 * (i + k)]),
+                                         __uint_as_float(v[c & 1][2 * (i + k) + 1])),
+                             sc[k], acc[c * 8 + i + k]);
           }
         }
         if (ROWB) {
