@@ -8,6 +8,7 @@
 #include <algorithm>
 #include <climits>
 #include <cmath>
+#include <cstdlib>
 
 #include "dcn_block_norm.cuh"
 #include "dcn_host.h"
@@ -267,6 +268,8 @@ dcn_status dcn_core_block_norm_backward(
   a.grad_y = grad_branch;
   a.s_part = s_sums ? ws : nullptr;
   a.t_part = t_sums ? ws + split.s_floats : nullptr;
+  const char* stall = std::getenv("DCN_CORE_TEST_STALL");
+  a.inject_stall = stall != nullptr && std::atoi(stall) == 1;
   a.error_word = dev.error_word;
   st = with_types(norm, [&](auto s, auto b) {
     return with_mapping((int64_t(a.C) + 3) / 4, vector_rows(norm), [&](auto tpr, auto v) {

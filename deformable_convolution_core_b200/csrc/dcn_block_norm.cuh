@@ -498,6 +498,7 @@ struct NormBwdArgs {
   const void* grad_h;
   void* grad_x;
   void* grad_y;
+  int inject_stall;  // test knob: 1 = a CTA's first rows never arrive, so the waits expire
   float* s_part;  // (ctas + gates - 1, 2, C): S1, S0 of each meeting pair, or null
   float* t_part;  // (ctas, 2, C): sums of dh * m and dh, or null
   unsigned int* error_word;
@@ -650,6 +651,7 @@ __global__ void __launch_bounds__(kNormBwdThreads, 1)
         const int i = int(it % S::kStages);
         const uint32_t u = it / S::kStages;
         if (u > 0 && !wait(&empty[i], (u - 1) & 1)) break;
+        if (a.inject_stall && it == 0) continue;  // test knob
         const int rows = int(min(int64_t(kRows), st.seg_end - st.base));
         const NormCopy cs = norm_copy(st.base, rows, a.C, sizeof(TS), total * sizeof(TS));
         const NormCopy cb = norm_copy(st.base, rows, a.C, sizeof(TB), total * sizeof(TB));
@@ -681,7 +683,8 @@ __global__ void __launch_bounds__(kNormBwdThreads, 1)
       }
       // the copies of the last issued stages may still be landing
       for (uint32_t j = it > uint32_t(S::kStages) ? it - S::kStages : 0; j < it; ++j)
-        (void)mbar_wait_bounded(&full[j % S::kStages], (j / S::kStages) & 1);
+        if (!(a.inject_stall && j == 0))
+          (void)mbar_wait_bounded(&full[j % S::kStages], (j / S::kStages) & 1);
     }
     return;
   }

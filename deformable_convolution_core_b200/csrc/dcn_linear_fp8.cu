@@ -9,6 +9,7 @@
 
 #include <algorithm>
 #include <climits>
+#include <cstdlib>
 #include <cstring>
 
 #include "dcn_fp8.cuh"
@@ -248,6 +249,8 @@ dcn_status linear(const void* a, const float* sa, int M, int K, const void* b, c
   g.out = split ? workspace : out;
   g.out_pitch = split ? p.part_pitch : N;
   g.tma_out = (int64_t(g.out_pitch) * esize(kernel_dtype)) % 16 == 0;
+  const char* stall = std::getenv("DCN_CORE_TEST_STALL");
+  g.inject_stall = stall != nullptr && std::atoi(stall) == 1;
   g.error_word = dev.error_word;
   CUtensorMap amap, bmap, omap;
   std::memset(&omap, 0, sizeof(omap));

@@ -72,6 +72,7 @@ struct LinearArgs {
   void* out;               // (splits, M, out_pitch) values of the output type
   int out_pitch;
   int tma_out;             // 1: rows are multiples of 16 bytes, stored by TMA
+  int inject_stall;        // test knob: 1 = never load a CTA's first stage, so the waits expire
   unsigned int* error_word;
 };
 
@@ -313,6 +314,7 @@ __global__ void __launch_bounds__(kLfThreads, 1)
             stop = true;
             break;
           }
+          if (a.inject_stall && issued == 0) continue;  // test knob
           mbar_arrive_expect_tx(&full[r.slot], S::kStageBytes);
           tma_load_2d(stage_a + r.slot * (kLfBM * kLfBK), &amap, &full[r.slot], kb * kLfBK, w.m0);
           tma_load_2d(stage_b + r.slot * (BN * kLfBK), &bmap, &full[r.slot], kb * kLfBK, w.n0);
@@ -320,7 +322,8 @@ __global__ void __launch_bounds__(kLfThreads, 1)
       }
       // the copies of the last issued stages may still be landing
       for (uint32_t j = issued > uint32_t(S::kStages) ? issued - S::kStages : 0; j < issued; ++j)
-        (void)mbar_wait_bounded(&full[j % S::kStages], (j / S::kStages) & 1);
+        if (!(a.inject_stall && j == 0))
+          (void)mbar_wait_bounded(&full[j % S::kStages], (j / S::kStages) & 1);
     }
   } else if (warp == 1 || warp == 3) {
     // ---- MMA issuers: every other K block, one accumulator a block ----
@@ -528,14 +531,21 @@ __global__ void __launch_bounds__(kLfThreads, 1)
           }
         } else {
           __syncwarp();
-          const size_t out0 = (size_t(split) * a.M + size_t(r0)) * a.out_pitch + col0 + c * kCols;
-          for (int e = lane; e < rows * kCols; e += 32) {
-            const int r = e / kCols, j = e % kCols, byte = j * int(sizeof(T));
-            const T x = *reinterpret_cast<const T*>(buf + unit_at(r, byte >> 4) + (byte & 15));
-            const size_t o = out0 + size_t(r) * a.out_pitch + j;
-            if (c * kCols + j < cols &&
-                in_range_of(a.error_word, o, 1, size_t(a.splits) * a.M * a.out_pitch))
-              static_cast<T*>(a.out)[o] = x;
+          // rows that no vector or TMA store can start: a lane's columns of one row after
+          // the other, so that a warp's stores are one run of the row
+          size_t o = (size_t(split) * a.M + size_t(r0)) * a.out_pitch + col0 + c * kCols + lane;
+          const size_t total = size_t(a.splits) * a.M * a.out_pitch;
+          constexpr int kLaneCols = kCols / 32;
+          const int left = cols - c * kCols - lane;
+#pragma unroll 8
+          for (int r = 0; r < 32; ++r, o += a.out_pitch) {
+#pragma unroll
+            for (int k = 0; k < kLaneCols; ++k) {
+              const int byte = (lane + 32 * k) * int(sizeof(T));
+              const T x = *reinterpret_cast<const T*>(buf + unit_at(r, byte >> 4) + (byte & 15));
+              if (r < rows && 32 * k < left && in_range_of(a.error_word, o + 32 * k, 1, total))
+                static_cast<T*>(a.out)[o + 32 * k] = x;
+            }
           }
         }
       }
