@@ -451,6 +451,20 @@ __global__ void __launch_bounds__(kLfThreads, 1)
       }
       w.next(a);
       fetch_bias();
+      if (cols <= 0) {  // a last column tile that ends before this warp's columns
+        for (int kb = 0; kb < kbs; ++kb, t.next(), sr.next()) {
+          if (!mbar_wait_watch(tfull_a + 8 * t.slot, t.phase, abort_flag)) {
+            give_up();
+            stop = true;
+            break;
+          }
+          if (lane == 0) {
+            mbar_arrive_at(tempty_a + 8 * t.slot);
+            mbar_arrive_at(sempty_a + 8 * sr.slot);
+          }
+        }
+        continue;
+      }
       for (int kb = 0; kb < kbs; ++kb, t.next(), sr.next()) {
         const float* s_col = col_scale + sr.slot * S::kScaleFloats;
         const uint32_t s_done = sempty_a + 8 * sr.slot;
