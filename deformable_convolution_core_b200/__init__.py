@@ -389,7 +389,7 @@ def _torch_types() -> dict:
         import torch
         _TORCH.update({DCN_F32: (torch.float32,), DCN_BF16: (torch.bfloat16,),
                        DCN_F16: (torch.float16,), "codes": (torch.float8_e4m3fn, torch.uint8),
-                       "device": torch.cuda.current_device,
+                       "device": getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
                        "stream": torch.cuda.current_stream,
                        "raw_stream": getattr(torch._C, "_cuda_getCurrentRawStream", None)})
     return _TORCH
@@ -407,52 +407,53 @@ def _bad_arg(t, name: str, numel: int, dtypes):
     raise ValueError(f"{name}: expected {numel} elements, got {t.numel()}")
 
 
-class _Args:
-    """Checks and converts the tensors of one call of the block operators: each must
-    be contiguous, on the current device, of the named type and of exactly the
-    number of elements that the sizes give (another size means that two tensors
-    were mixed up).  None and raw addresses go through as they are."""
-    __slots__ = ("types", "device")
+def _here() -> int | None:
+    """The current CUDA device, or None without one."""
+    try:
+        return _torch_types()["device"]()
+    except (AssertionError, RuntimeError):
+        return None
 
-    def __init__(self):
-        self.types = _TORCH or _torch_types()
-        self.device = None
 
-    def __call__(self, t, name: str, numel: int, kind) -> int | None:
-        if t is None or type(t) is int:
+# The tensors of one call of the block operators are checked and converted one by one:
+# each must be contiguous, on the current device, of the named type and of exactly the
+# number of elements that the sizes give (another size means that two tensors were
+# mixed up).  None and raw addresses go through as they are.  A plain function: a call
+# has up to 19 of them, and a short kernel ends before their checks do.
+def _arg(t, name: str, numel: int, kind, device) -> int | None:
+    if t is None:
+        return None
+    try:
+        if (t.get_device() == device and t.dtype in _TORCH[kind] and t.numel() == numel
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except (AttributeError, TypeError, KeyError):
+        if type(t) is int:
             return t
-        try:
-            if (t.get_device() == self.device and t.numel() == numel
-                    and t.dtype in self.types[kind] and t.is_contiguous()):
-                return t.data_ptr()
-            if self.device is None and t.is_cuda:
-                self.device = self.types["device"]()
-                return self(t, name, numel, kind)
-        except (AttributeError, TypeError, KeyError):
-            pass
-        _bad_arg(t, name, numel, self.types.get(kind, ()))
+    _bad_arg(t, name, numel, _TORCH.get(kind, ()))
 
-    def workspace(self, t, nbytes: int) -> int | None:
-        if t is None or type(t) is int:
-            return t
-        if t.numel() * t.element_size() < nbytes:
-            raise ValueError(f"workspace: {nbytes} bytes named, the tensor has "
-                             f"{t.numel() * t.element_size()}")
-        if not t.is_contiguous() or not t.is_cuda or t.get_device() != self.types["device"]():
-            _bad_arg(t, "workspace", t.numel(), None)
-        return t.data_ptr()
 
-    def stream(self, s) -> int | None:
-        if s is not None:
-            return s if type(s) is int else s.cuda_stream
-        raw = self.types["raw_stream"]
-        if raw is not None:
-            return raw(self.types["device"]() if self.device is None else self.device)
-        return self.types["stream"]().cuda_stream
+def _arg_workspace(t, nbytes: int, device) -> int | None:
+    if t is None or type(t) is int:
+        return t
+    if t.nbytes < nbytes:
+        raise ValueError(f"workspace: {nbytes} bytes named, the tensor has {t.nbytes}")
+    if not t.is_contiguous() or t.get_device() != device:
+        _bad_arg(t, "workspace", t.numel(), None)
+    return t.data_ptr()
+
+
+def _arg_stream(s, device) -> int | None:
+    if s is not None:
+        return s if type(s) is int else s.cuda_stream
+    raw = _TORCH["raw_stream"]
+    if raw is None or device is None:
+        return _TORCH["stream"]().cuda_stream
+    return raw(device)
 
 
 def _ceil(a: int, b: int) -> int:
-    return -(-int(a) // b)
+    return -(-a // b)
 
 
 def dcn_core_fp8_pitch(cols: int) -> int:
@@ -472,13 +473,14 @@ def dcn_core_quantize_fp8(input, rows: int, cols: int, dtype, block_rows: int, q
     rows, cols = int(rows), int(cols)
     kb, mb = _ceil(cols, 128), _ceil(rows, 128)
     whole = block_rows == 128
-    arg = _Args()
+    here = _here()
     _check(load_library().dcn_core_quantize_fp8(
-        arg(input, "input", rows * cols, dtype), dtype, rows, cols, block_rows,
-        arg(q, "q", rows * _ceil(cols, 16) * 16, "codes"),
-        arg(scales, "scales", kb * (mb if whole else rows), DCN_F32),
-        arg(q_t, "q_t", cols * _ceil(rows, 16) * 16, "codes"),
-        arg(scales_t, "scales_t", mb * (kb if whole else cols), DCN_F32), arg.stream(stream)),
+        _arg(input, "input", rows * cols, dtype, here), dtype, rows, cols, block_rows,
+        _arg(q, "q", rows * _ceil(cols, 16) * 16, "codes", here),
+        _arg(scales, "scales", kb * (mb if whole else rows), DCN_F32, here),
+        _arg(q_t, "q_t", cols * _ceil(rows, 16) * 16, "codes", here),
+        _arg(scales_t, "scales_t", mb * (kb if whole else cols), DCN_F32, here),
+        _arg_stream(stream, here)),
         "dcn_core_quantize_fp8")
 
 
@@ -496,13 +498,16 @@ def dcn_core_linear_fp8(input, input_scales, M: int, K: int, weight, weight_scal
         out_dtype = DTYPES[out_dtype]
     M, K, Nout = int(M), int(K), int(Nout)
     kb, pitch = _ceil(K, 128), _ceil(K, 16) * 16
-    arg = _Args()
+    here = _here()
     _check(load_library().dcn_core_linear_fp8(
-        arg(input, "input", M * pitch, "codes"), arg(input_scales, "input_scales", kb * M, DCN_F32),
-        M, K, arg(weight, "weight", Nout * pitch, "codes"),
-        arg(weight_scales, "weight_scales", kb * _ceil(Nout, 128), DCN_F32), Nout,
-        arg(bias, "bias", Nout, DCN_F32), arg(output, "output", M * Nout, out_dtype), out_dtype,
-        arg.workspace(workspace, workspace_bytes), workspace_bytes, arg.stream(stream)),
+        _arg(input, "input", M * pitch, "codes", here),
+        _arg(input_scales, "input_scales", kb * M, DCN_F32, here),
+        M, K, _arg(weight, "weight", Nout * pitch, "codes", here),
+        _arg(weight_scales, "weight_scales", kb * _ceil(Nout, 128), DCN_F32, here), Nout,
+        _arg(bias, "bias", Nout, DCN_F32, here), _arg(output, "output", M * Nout, out_dtype, here),
+        out_dtype,
+        _arg_workspace(workspace, workspace_bytes, here),
+        workspace_bytes, _arg_stream(stream, here)),
         "dcn_core_linear_fp8")
 
 
@@ -522,17 +527,18 @@ def dcn_core_linear_fp8_backward(grad_out, dtype, M: int, K: int, Nout: int, wei
         dtype = DTYPES[dtype]
     M, K, Nout = int(M), int(K), int(Nout)
     nb, mb = _ceil(Nout, 128), _ceil(M, 128)
-    arg = _Args()
+    here = _here()
     _check(load_library().dcn_core_linear_fp8_backward(
-        arg(grad_out, "grad_out", M * Nout, dtype), dtype, M, K, Nout,
-        arg(weight_t, "weight_t", K * _ceil(Nout, 16) * 16, "codes"),
-        arg(weight_t_scales, "weight_t_scales", nb * _ceil(K, 128), DCN_F32),
-        arg(input_t, "input_t", K * _ceil(M, 16) * 16, "codes"),
-        arg(input_t_scales, "input_t_scales", mb * K, DCN_F32),
-        arg(grad_input, "grad_input", M * K, dtype),
-        arg(grad_weight, "grad_weight", Nout * K, DCN_F32),
-        arg(grad_bias, "grad_bias", Nout, DCN_F32), arg.workspace(workspace, workspace_bytes),
-        workspace_bytes, arg.stream(stream)), "dcn_core_linear_fp8_backward")
+        _arg(grad_out, "grad_out", M * Nout, dtype, here), dtype, M, K, Nout,
+        _arg(weight_t, "weight_t", K * _ceil(Nout, 16) * 16, "codes", here),
+        _arg(weight_t_scales, "weight_t_scales", nb * _ceil(K, 128), DCN_F32, here),
+        _arg(input_t, "input_t", K * _ceil(M, 16) * 16, "codes", here),
+        _arg(input_t_scales, "input_t_scales", mb * K, DCN_F32, here),
+        _arg(grad_input, "grad_input", M * K, dtype, here),
+        _arg(grad_weight, "grad_weight", Nout * K, DCN_F32, here),
+        _arg(grad_bias, "grad_bias", Nout, DCN_F32, here),
+        _arg_workspace(workspace, workspace_bytes, here),
+        workspace_bytes, _arg_stream(stream, here)), "dcn_core_linear_fp8_backward")
 
 
 def dcn_core_block_norm(norm: DcnBlockNorm, residual, branch, gate, post_gamma, post_beta,
@@ -544,16 +550,21 @@ def dcn_core_block_norm(norm: DcnBlockNorm, residual, branch, gate, post_gamma, 
     M, C, sd, bd = norm.M, norm.C, norm.stream_dtype, norm.branch_dtype
     gates = _ceil(M, norm.rows_per_gate) if norm.rows_per_gate > 0 else 1
     fp8 = normed_scales is not None
-    arg = _Args()
+    here = _here()
     _check(load_library().dcn_core_block_norm(
-        ctypes.byref(norm), arg(residual, "residual", M * C, sd), arg(branch, "branch", M * C, bd),
-        arg(gate, "gate", gates * C, DCN_F32), arg(post_gamma, "post_gamma", C, DCN_F32),
-        arg(post_beta, "post_beta", C, DCN_F32), arg(pre_gamma, "pre_gamma", C, DCN_F32),
-        arg(pre_beta, "pre_beta", C, DCN_F32), arg(residual_out, "residual_out", M * C, sd),
-        arg(normed, "normed", M * (_ceil(C, 16) * 16 if fp8 else C), "codes" if fp8 else bd),
-        arg(normed_scales, "normed_scales", _ceil(C, 128) * M, DCN_F32),
-        arg(post_stats, "post_stats", 2 * M, DCN_F32), arg(pre_stats, "pre_stats", 2 * M, DCN_F32),
-        arg.stream(stream)), "dcn_core_block_norm")
+        ctypes.byref(norm), _arg(residual, "residual", M * C, sd, here),
+        _arg(branch, "branch", M * C, bd, here),
+        _arg(gate, "gate", gates * C, DCN_F32, here),
+        _arg(post_gamma, "post_gamma", C, DCN_F32, here),
+        _arg(post_beta, "post_beta", C, DCN_F32, here),
+        _arg(pre_gamma, "pre_gamma", C, DCN_F32, here),
+        _arg(pre_beta, "pre_beta", C, DCN_F32, here),
+        _arg(residual_out, "residual_out", M * C, sd, here),
+        _arg(normed, "normed", M * (_ceil(C, 16) * 16 if fp8 else C), "codes" if fp8 else bd, here),
+        _arg(normed_scales, "normed_scales", _ceil(C, 128) * M, DCN_F32, here),
+        _arg(post_stats, "post_stats", 2 * M, DCN_F32, here),
+        _arg(pre_stats, "pre_stats", 2 * M, DCN_F32, here),
+        _arg_stream(stream, here)), "dcn_core_block_norm")
 
 
 def dcn_core_block_norm_backward_workspace(norm: DcnBlockNorm) -> int:
@@ -570,21 +581,26 @@ def dcn_core_block_norm_backward(norm: DcnBlockNorm, residual_out, branch, gate,
     as None is not computed."""
     M, C, sd, bd = norm.M, norm.C, norm.stream_dtype, norm.branch_dtype
     gates = _ceil(M, norm.rows_per_gate) if norm.rows_per_gate > 0 else 1
-    arg = _Args()
+    here = _here()
     _check(load_library().dcn_core_block_norm_backward(
-        ctypes.byref(norm), arg(residual_out, "residual_out", M * C, sd),
-        arg(branch, "branch", M * C, bd), arg(gate, "gate", gates * C, DCN_F32),
-        arg(post_gamma, "post_gamma", C, DCN_F32), arg(post_beta, "post_beta", C, DCN_F32),
-        arg(pre_gamma, "pre_gamma", C, DCN_F32), arg(post_stats, "post_stats", 2 * M, DCN_F32),
-        arg(pre_stats, "pre_stats", 2 * M, DCN_F32),
-        arg(grad_residual_out, "grad_residual_out", M * C, sd),
-        arg(grad_normed, "grad_normed", M * C, bd), arg(grad_residual, "grad_residual", M * C, sd),
-        arg(grad_branch, "grad_branch", M * C, bd), arg(grad_gate, "grad_gate", gates * C, DCN_F32),
-        arg(grad_post_gamma, "grad_post_gamma", C, DCN_F32),
-        arg(grad_post_beta, "grad_post_beta", C, DCN_F32),
-        arg(grad_pre_gamma, "grad_pre_gamma", C, DCN_F32),
-        arg(grad_pre_beta, "grad_pre_beta", C, DCN_F32),
-        arg.workspace(workspace, workspace_bytes), workspace_bytes, arg.stream(stream)),
+        ctypes.byref(norm), _arg(residual_out, "residual_out", M * C, sd, here),
+        _arg(branch, "branch", M * C, bd, here), _arg(gate, "gate", gates * C, DCN_F32, here),
+        _arg(post_gamma, "post_gamma", C, DCN_F32, here),
+        _arg(post_beta, "post_beta", C, DCN_F32, here),
+        _arg(pre_gamma, "pre_gamma", C, DCN_F32, here),
+        _arg(post_stats, "post_stats", 2 * M, DCN_F32, here),
+        _arg(pre_stats, "pre_stats", 2 * M, DCN_F32, here),
+        _arg(grad_residual_out, "grad_residual_out", M * C, sd, here),
+        _arg(grad_normed, "grad_normed", M * C, bd, here),
+        _arg(grad_residual, "grad_residual", M * C, sd, here),
+        _arg(grad_branch, "grad_branch", M * C, bd, here),
+        _arg(grad_gate, "grad_gate", gates * C, DCN_F32, here),
+        _arg(grad_post_gamma, "grad_post_gamma", C, DCN_F32, here),
+        _arg(grad_post_beta, "grad_post_beta", C, DCN_F32, here),
+        _arg(grad_pre_gamma, "grad_pre_gamma", C, DCN_F32, here),
+        _arg(grad_pre_beta, "grad_pre_beta", C, DCN_F32, here),
+        _arg_workspace(workspace, workspace_bytes, here),
+        workspace_bytes, _arg_stream(stream, here)),
         "dcn_core_block_norm_backward")
 
 
