@@ -81,7 +81,7 @@ def hbm_peak():
 # Sources of the kernels the bench step launches: every file under csrc/ except
 # those that only define kernels the step never runs.
 OTHER_KERNEL_SOURCES = ("dcn_guide.cuh", "dcn_guide_projection.cuh", "dcn_projection.cuh",
-                        "dcn_block_norm.cu", "dcn_block_norm.cuh", "dcn_fp8.cuh",
+                        "dcn_block_norm.cu", "dcn_block_norm.cuh", "dcn_chain.cuh", "dcn_fp8.cuh",
                         "dcn_linear_fp8.cu", "dcn_linear_fp8.cuh", "dcn_quantize.cuh")
 
 

@@ -305,8 +305,8 @@ dcn_status dcn_core_block_norm_backward(
   f.grad_post_beta = grad_post_beta;
   f.grad_pre_gamma = grad_pre_gamma;
   f.grad_pre_beta = grad_pre_beta;
-  dcn_block_norm_sums_kernel<<<dim3(unsigned((a.C + 31) / 32), 2), 32 * kSumGroups, 0, stream>>>(f);
-  return launched();
+  return launch_kernel(dcn_block_norm_sums_kernel, true, dim3(unsigned((a.C + 31) / 32), 2),
+                       32 * kSumGroups, 0, stream, f);
 }
 
 }  // extern "C"

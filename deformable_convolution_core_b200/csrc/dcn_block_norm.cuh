@@ -13,6 +13,7 @@
 
 #include <type_traits>
 
+#include "dcn_chain.cuh"
 #include "dcn_fp8.cuh"
 #include "dcn_ptx.cuh"
 
@@ -614,6 +615,7 @@ struct NormBwdShape {
 template <typename TS, typename TB, int TPR, bool VEC, bool FULL>
 __global__ void __launch_bounds__(kNormBwdThreads, 1)
     dcn_block_norm_backward_kernel(const NormBwdArgs a) {
+  chain_release();
   using S = NormBwdShape<TS, TB>;
   extern __shared__ __align__(128) unsigned char nb_smem[];
   __shared__ float2 s_slots[2 * (kNormThreads / 32)];
@@ -895,6 +897,7 @@ __device__ __forceinline__ float2 join_groups(float2 v, int g, float2 (*s)[32]) 
 // those of dh (blockIdx.y = 1), are.
 __global__ void __launch_bounds__(32 * kSumGroups)
     dcn_block_norm_sums_kernel(const NormSumArgs a) {
+  chain_wait();
   __shared__ float2 s[kSumGroups][32];
   const int c = int(blockIdx.x) * 32 + int(threadIdx.x & 31), g = int(threadIdx.x >> 5);
   const bool in = c < a.C;

@@ -12,6 +12,7 @@
 #include <cstdlib>
 #include <cstring>
 
+#include "dcn_chain.cuh"
 #include "dcn_fp8.cuh"
 #include "dcn_host.h"
 #include "dcn_linear_fp8.cuh"
@@ -191,7 +192,7 @@ dcn_status out_map(CUtensorMap* map, void* base, dcn_dtype dtype, int N, int pit
 
 template <typename T, int BN, bool ROWB>
 dcn_status launch_linear(const CUtensorMap& amap, const CUtensorMap& bmap, const CUtensorMap& omap,
-                         LinearArgs args, int sms, cudaStream_t stream) {
+                         LinearArgs args, int sms, bool follows, cudaStream_t stream) {
   auto k = dcn_linear_fp8_kernel<T, BN, ROWB>;
   constexpr size_t smem = LfShape<BN>::kSmemBytes;
   if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) !=
@@ -200,14 +201,15 @@ dcn_status launch_linear(const CUtensorMap& amap, const CUtensorMap& bmap, const
   const int grid = std::min(args.items, sms);
   args.step_n = grid % args.n_tiles;
   args.step_m = grid / args.n_tiles;
-  k<<<unsigned(grid), kLfThreads, smem, stream>>>(amap, bmap, omap, args);
-  return launched();
+  return launch_kernel(k, follows, dim3(unsigned(grid)), kLfThreads, smem, stream, amap, bmap, omap,
+                       args);
 }
 
-// out (M, N) = A (M, K) B (N, K)^T with the blocks' scales, + bias.
+// out (M, N) = A (M, K) B (N, K)^T with the blocks' scales, + bias.  follows: another kernel
+// of the call is before it on the stream.
 dcn_status linear(const void* a, const float* sa, int M, int K, const void* b, const float* sb,
                   bool row_scales, int N, const float* bias, void* out, dcn_dtype out_dtype,
-                  void* workspace, size_t workspace_bytes, const DeviceInfo& dev,
+                  void* workspace, size_t workspace_bytes, const DeviceInfo& dev, bool follows,
                   cudaStream_t stream) {
   const LinearPlan p = linear_plan(M, K, N, row_scales, dev.sms);
   const int64_t pitch = pitch_of(K);
@@ -227,8 +229,7 @@ dcn_status linear(const void* a, const float* sa, int M, int K, const void* b, c
       using T = decltype(tag);
       const int64_t columns = kLrWarps / r.wk * 8;
       const unsigned grid = unsigned((int64_t(N) + columns - 1) / columns);
-      dcn_linear_fp8_rows_kernel<T><<<grid, kLrThreads, 0, stream>>>(r);
-      return launched();
+      return launch_kernel(dcn_linear_fp8_rows_kernel<T>, follows, dim3(grid), kLrThreads, 0, stream, r);
     });
   }
   const size_t need = plan_workspace(p, M);
@@ -262,19 +263,18 @@ dcn_status linear(const void* a, const float* sa, int M, int K, const void* b, c
   st = with_storage(kernel_dtype, [&](auto tag) {
     using T = decltype(tag);
     if (row_scales)
-      return p.bn == 256 ? launch_linear<T, 256, true>(amap, bmap, omap, g, dev.sms, stream)
-                         : launch_linear<T, 128, true>(amap, bmap, omap, g, dev.sms, stream);
-    return p.bn == 256 ? launch_linear<T, 256, false>(amap, bmap, omap, g, dev.sms, stream)
-                       : launch_linear<T, 128, false>(amap, bmap, omap, g, dev.sms, stream);
+      return p.bn == 256 ? launch_linear<T, 256, true>(amap, bmap, omap, g, dev.sms, follows, stream)
+                         : launch_linear<T, 128, true>(amap, bmap, omap, g, dev.sms, follows, stream);
+    return p.bn == 256 ? launch_linear<T, 256, false>(amap, bmap, omap, g, dev.sms, follows, stream)
+                       : launch_linear<T, 128, false>(amap, bmap, omap, g, dev.sms, follows, stream);
   });
   if (st != DCN_OK || !split) return st;
   return with_storage(out_dtype, [&](auto tag) {
     using T = decltype(tag);
     const int64_t grid = std::min<int64_t>((int64_t(M) * N + 255) / 256, int64_t(dev.sms) * 16);
-    dcn_linear_join_kernel<T><<<unsigned(grid), 256, 0, stream>>>(
-        static_cast<const float*>(workspace), p.splits, M, N, p.part_pitch, bias,
-        static_cast<T*>(out));
-    return launched();
+    return launch_kernel(dcn_linear_join_kernel<T>, true, dim3(unsigned(grid)), 256, 0, stream,
+                         static_cast<const float*>(workspace), p.splits, M, N, p.part_pitch, bias,
+                         static_cast<T*>(out));
   });
 }
 
@@ -357,7 +357,7 @@ dcn_status dcn_core_linear_fp8(const void* input, const float* input_scales, int
   DeviceInfo dev;
   if (device_info(&dev) != DCN_OK) return DCN_ERR_CUDA;
   return linear(input, input_scales, M, K, weight, weight_scales, false, Nout, bias, output,
-                out_dtype, workspace, workspace_bytes, dev, stream);
+                out_dtype, workspace, workspace_bytes, dev, false, stream);
 }
 
 size_t dcn_core_linear_fp8_backward_workspace(int M, int K, int Nout) {
@@ -401,18 +401,17 @@ dcn_status dcn_core_linear_fp8_backward(const void* grad_out, dcn_dtype dtype, i
                            grad_weight ? scales_t : nullptr, grad_bias ? col_sums : nullptr,
                            dev.error_word, stream);
   if (st != DCN_OK) return st;
-  if (grad_bias) {
-    dcn_column_sum_kernel<<<unsigned((int64_t(Nout) + 31) / 32), 256, 0, stream>>>(
-        col_sums, blocks_of(M), Nout, grad_bias);
-    if ((st = launched()) != DCN_OK) return st;
-  }
+  if (grad_bias &&
+      (st = launch_kernel(dcn_column_sum_kernel, true, dim3(unsigned((int64_t(Nout) + 31) / 32)), 256,
+                          0, stream, col_sums, blocks_of(M), Nout, grad_bias)) != DCN_OK)
+    return st;
   if (grad_input &&
       (st = linear(ws + l.q, scales, M, Nout, weight_t, weight_t_scales, false, K, nullptr,
-                   grad_input, dtype, ws + l.part, part_bytes, dev, stream)) != DCN_OK)
+                   grad_input, dtype, ws + l.part, part_bytes, dev, true, stream)) != DCN_OK)
     return st;
   if (grad_weight &&
       (st = linear(ws + l.q_t, scales_t, Nout, M, input_t, input_t_scales, true, K, nullptr,
-                   grad_weight, DCN_F32, ws + l.part, part_bytes, dev, stream)) != DCN_OK)
+                   grad_weight, DCN_F32, ws + l.part, part_bytes, dev, true, stream)) != DCN_OK)
     return st;
   return DCN_OK;
 }

@@ -34,6 +34,7 @@
 
 #include <cuda.h>
 
+#include "dcn_chain.cuh"
 #include "dcn_fp8.cuh"
 #include "dcn_ptx.cuh"
 
@@ -297,6 +298,8 @@ __global__ void __launch_bounds__(kLfThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  chain_wait();
+  chain_release();
   volatile int* abort_flag = s_abort;
   auto give_up = [&]() {
     atomicOr(a.error_word, kErrTimeout);
@@ -588,6 +591,8 @@ template <typename T>
 __global__ void __launch_bounds__(256)
     dcn_linear_join_kernel(const float* part, int splits, int M, int N, int pitch,
                            const float* bias, T* out) {
+  chain_wait();
+  chain_release();
   const size_t plane = size_t(M) * pitch, n = size_t(M) * N;
   for (size_t i = size_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += size_t(gridDim.x) * 256) {
     const size_t m = i / unsigned(N);
@@ -658,6 +663,8 @@ __device__ __forceinline__ void load_codes(const uint8_t* row, bool in, int k, i
 template <typename T>
 __global__ void __launch_bounds__(kLrThreads)
     dcn_linear_fp8_rows_kernel(const LinearRowsArgs a) {
+  chain_wait();
+  chain_release();
   __shared__ float red[kLrWarps][8][8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;

@@ -1,6 +1,7 @@
 // Quantiser to block-scaled e4m3 (dcn_fp8.cuh).
 #pragma once
 
+#include "dcn_chain.cuh"
 #include "dcn_fp8.cuh"
 #include "dcn_ptx.cuh"
 
@@ -98,6 +99,7 @@ constexpr int kQuantThreads = 256;
 template <typename T, bool VEC, bool WHOLE, bool ROWS, bool TRANS, bool SUMS>
 __global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 ? 3 : 2)
     dcn_quantize_kernel(const QuantArgs a) {
+  chain_release();
   using E = Eight<T>;
   constexpr int kW = E::kWords;
   __shared__ uint32_t s_top[8][16][kW];          // per warp and 8 columns: magnitudes
@@ -295,6 +297,8 @@ __global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 ? 3 : 2)
 // 8 threads a column.
 __global__ void __launch_bounds__(256) dcn_column_sum_kernel(const float* part, int tiles,
                                                              int cols, float* out) {
+  chain_wait();
+  chain_release();
   __shared__ float s[8][33];
   const int c = int(blockIdx.x) * 32 + int(threadIdx.x & 31), g = int(threadIdx.x >> 5);
   float v = 0.f;
