@@ -75,7 +75,7 @@ dcn_status launch_backward(Kernel k, size_t smem, const NormBwdArgs& a, int ctas
   if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) !=
       cudaSuccess)
     return DCN_ERR_CUDA;
-  k<<<unsigned(ctas), kNormBwdThreads, smem, stream>>>(a);
+  k<<<unsigned(ctas), kNormThreads, smem, stream>>>(a);
   return launched();
 }
 

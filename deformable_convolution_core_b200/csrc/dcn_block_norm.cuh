@@ -506,7 +506,7 @@ struct NormBwdArgs {
   unsigned int* error_word;
 };
 
-// The barrier of the eight working warps (the copying warp has no part in it).
+// The barrier of the CTA's eight warps (0 to 8 are the rows').
 __device__ __forceinline__ void norm_sync() {
   asm volatile("bar.sync 9, %0;" ::"n"(kNormThreads) : "memory");
 }
@@ -593,7 +593,6 @@ __device__ __forceinline__ NormCopy norm_copy(int64_t base, int rows, int C, int
   return c;
 }
 
-constexpr int kNormBwdThreads = kNormThreads + 32;  // eight working warps and the copying one
 template <typename TS, typename TB>
 struct NormBwdShape {
   // A step's rows have at most kNormMaxC values; 32 bytes for the shift and the end.
@@ -605,15 +604,18 @@ struct NormBwdShape {
   static constexpr size_t kSmemBytes = size_t(kStages) * kStageBytes + kParamBytes + 128;
 };
 
-// Eight working warps keep the four running sums of their channels (80 registers a
-// thread) and a row's normalised values and gradients (40); a ninth warp copies the
-// steps' rows into a ring in shared memory, so that what is in flight does not depend
-// on registers.  pre_gamma and gate * post_gamma of the rows at hand stand in shared
-// memory too, ones where there are none.  It takes about 30 instructions a value, which
-// eight warps issue in 37% of the slots, each waiting on the sums of its row: 127 us for
-// 147,456 x 320 bf16 with gates and both norms, 4.5 TB/s (68% of the copy rate).
+// Eight warps keep the four running sums of their channels (80 registers a thread) and
+// a row's normalised values and gradients (40); the warps in turn have the steps' rows
+// copied into a ring in shared memory, so that what is in flight does not depend on registers.  (A
+// ninth warp for the copies would leave 168 registers to each, by the granularity of
+// their allocation, and spill where a width leaves threads without channels: 41 us for
+// 4001 x 773 fp32 against 34.  One thread of one warp for all copies: 129 us at 320.)
+// pre_gamma and gate * post_gamma of the rows at hand stand in shared
+// memory too, ones where there are none.  Each step is a chain of waits (the rows, two
+// sums over a row, the stores): 107 us for 147,456 x 320 bf16 with gates and both norms,
+// 5.3 TB/s or 81% of the copy rate (124 with the rows' statistics loaded when needed).
 template <typename TS, typename TB, int TPR, bool VEC, bool FULL>
-__global__ void __launch_bounds__(kNormBwdThreads, 1)
+__global__ void __launch_bounds__(kNormThreads, 1)
     dcn_block_norm_backward_kernel(const NormBwdArgs a) {
   chain_release();
   using S = NormBwdShape<TS, TB>;
@@ -622,12 +624,15 @@ __global__ void __launch_bounds__(kNormBwdThreads, 1)
   __shared__ __align__(16) float s_buf[kNormMaxC];
   __shared__ uint64_t full[S::kStages], empty[S::kStages];
   __shared__ int s_abort;
+  __shared__ uint32_t s_copied;  // steps whose copies have been issued
   constexpr int kRows = kNormThreads / TPR;
   const int warp = int(threadIdx.x) >> 5, lane = int(threadIdx.x) & 31;
   volatile int* abort_flag = &s_abort;
+  volatile uint32_t* copied = &s_copied;
   if (threadIdx.x == 0) {
+    s_copied = 0;
     for (int i = 0; i < S::kStages; ++i) {
-      mbar_init(&full[i], 1);
+      mbar_init(&full[i], 4);
       mbar_init(&empty[i], kNormThreads / 32);
     }
     s_abort = 0;
@@ -644,54 +649,36 @@ __global__ void __launch_bounds__(kNormBwdThreads, 1)
     *abort_flag = 1;
     return false;
   };
-  if (warp == kNormThreads / 32) {
-    // ---- copies ----
-    if (lane == 0) {
-      const char* src[4] = {static_cast<const char*>(a.grad_r), static_cast<const char*>(a.r),
-                            static_cast<const char*>(a.grad_h), static_cast<const char*>(a.branch)};
-      if (a.pre == kNormNone) src[1] = src[2] = nullptr;
-      uint32_t it = 0;
-      for (NormSteps st(a); st.valid(); st.next(kRows), ++it) {
-        const int i = int(it % S::kStages);
-        const uint32_t u = it / S::kStages;
-        if (u > 0 && !wait(&empty[i], (u - 1) & 1)) break;
-        if (a.inject_stall && it == 0) continue;  // test knob
-        const int rows = int(min(int64_t(kRows), st.seg_end - st.base));
-        const NormCopy cs = norm_copy(st.base, rows, a.C, sizeof(TS), total * sizeof(TS));
-        const NormCopy cb = norm_copy(st.base, rows, a.C, sizeof(TB), total * sizeof(TB));
-        unsigned char* dst = nb_smem + size_t(i) * S::kStageBytes;
-        uint32_t bytes = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const NormCopy& c = k < 2 ? cs : cb;
-          if (src[k] == nullptr) continue;
-          if (!in_range_of(a.error_word, c.from, size_t(c.bytes) + c.tail,
-                           total * (k < 2 ? sizeof(TS) : sizeof(TB)))) {
-            src[k] = nullptr;  // the bounds-checked build: no copies of it from here on
-            continue;
-          }
-          bytes += c.bytes;
-          // the tensor's last bytes, fewer than a unit
-          unsigned char* d = dst + (k < 2 ? k * S::kTileS : 2 * S::kTileS + (k - 2) * S::kTileB);
-          for (uint32_t e = 0; e < c.tail; ++e)
-            d[c.bytes + e] = static_cast<unsigned char>(src[k][c.from + c.bytes + e]);
-        }
-        mbar_arrive_expect_tx(&full[i], bytes);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const NormCopy& c = k < 2 ? cs : cb;
-          if (src[k] == nullptr || c.bytes == 0) continue;
-          unsigned char* d = dst + (k < 2 ? k * S::kTileS : 2 * S::kTileS + (k - 2) * S::kTileB);
-          bulk_load(d, src[k] + c.from, c.bytes, &full[i]);
-        }
-      }
-      // the copies of the last issued stages may still be landing
-      for (uint32_t j = it > uint32_t(S::kStages) ? it - S::kStages : 0; j < it; ++j)
-        if (!(a.inject_stall && j == 0))
-          (void)mbar_wait_bounded(&full[j % S::kStages], (j / S::kStages) & 1);
-    }
-    return;
-  }
+  // ---- copies: the warps take the steps in turn, lanes 0 to 3 of one a tensor each ----
+  const bool of_branch = lane >= 2;
+  const int size = int(of_branch ? sizeof(TB) : sizeof(TS));
+  const char* src = static_cast<const char*>(lane == 0   ? a.grad_r
+                                             : lane == 1 ? a.r
+                                             : lane == 2 ? a.grad_h
+                                             : lane == 3 ? a.branch
+                                                         : nullptr);
+  if (a.pre == kNormNone && (lane == 1 || lane == 2)) src = nullptr;
+  const uint32_t src_at = of_branch ? 2 * S::kTileS + (lane & 1) * S::kTileB : (lane & 1) * S::kTileS;
+  auto copy_step = [&](const NormSteps& step, uint32_t n) {
+    if (lane >= 4 || (a.inject_stall && n == 0)) return;  // test knob
+    const int i = int(n % S::kStages);
+    const int rows = int(min(int64_t(kRows), step.seg_end - step.base));
+    const NormCopy c = norm_copy(step.base, rows, a.C, size, total * size);
+    if (src != nullptr &&
+        !in_range_of(a.error_word, c.from, size_t(c.bytes) + c.tail, total * size))
+      src = nullptr;  // the bounds-checked build: no copies of it from here on
+    const uint32_t bytes = src != nullptr ? c.bytes : 0;
+    unsigned char* d = nb_smem + size_t(i) * S::kStageBytes + src_at;
+    if (src != nullptr)  // the tensor's last bytes, fewer than a unit
+      for (uint32_t e = 0; e < c.tail; ++e)
+        d[c.bytes + e] = static_cast<unsigned char>(src[c.from + c.bytes + e]);
+    mbar_arrive_expect_tx(&full[i], bytes);
+    if (bytes > 0) bulk_load(d, src + c.from, bytes, &full[i]);
+    if (lane == 0) *copied = n + 1;
+  };
+  NormSteps next(a);  // the first step that is not copied yet
+  for (int i = 0; i < S::kStages && next.valid(); ++i, next.next(kRows))
+    if (warp == 0) copy_step(next, uint32_t(i));
   const int slot = int(threadIdx.x) / TPR, t = int(threadIdx.x) % TPR;
   float2* slots = s_slots + slot * 2 * (TPR / 32);
   int turn = 0;
@@ -718,11 +705,29 @@ __global__ void __launch_bounds__(kNormBwdThreads, 1)
 
   uint32_t it = 0;
   NormSteps st(a);
-  if (st.valid()) set_weight(st.gate);
+  auto row_at = [&](const NormSteps& s) { return min(s.base + slot, s.seg_end - 1); };
+  // a row's statistics, loaded a step ahead: their way from HBM would stand in every step
+  struct RowStats {
+    float m_mean, m_rstd, n_mean, n_rstd;
+  } ahead = {0.f, 0.f, 0.f, 1.f};
+  auto load_stats = [&](int64_t row) {
+    if (pre) {
+      ahead.m_mean = __ldg(a.pre_stats + row);
+      ahead.m_rstd = __ldg(a.pre_stats + size_t(a.M) + row);
+    }
+    if (post) {
+      ahead.n_mean = __ldg(a.post_stats + row);
+      ahead.n_rstd = __ldg(a.post_stats + size_t(a.M) + row);
+    }
+  };
+  if (st.valid()) {
+    load_stats(row_at(st));
+    set_weight(st.gate);
+  }
   while (st.valid()) {
     const int i = int(it % S::kStages);
     const bool live = st.base + slot < st.seg_end;
-    const int64_t row = live ? st.base + slot : st.seg_end - 1;
+    const int64_t row = row_at(st);
     const int at = int(row - st.base) * a.C;
     const size_t off = size_t(row) * a.C;
     const unsigned char* stage = nb_smem + size_t(i) * S::kStageBytes;
@@ -733,10 +738,10 @@ __global__ void __launch_bounds__(kNormBwdThreads, 1)
     const TS* x_r = reinterpret_cast<const TS*>(stage + S::kTileS + shift_s) + at;
     const TB* g_h = reinterpret_cast<const TB*>(stage + 2 * S::kTileS + shift_b) + at;
     const TB* y = reinterpret_cast<const TB*>(stage + 2 * S::kTileS + S::kTileB + shift_b) + at;
-    const float m_mean = pre ? __ldg(a.pre_stats + row) : 0.f;
-    const float m_rstd = pre ? __ldg(a.pre_stats + size_t(a.M) + row) : 0.f;
-    const float n_mean = post ? __ldg(a.post_stats + row) : 0.f;
-    const float n_rstd = post ? __ldg(a.post_stats + size_t(a.M) + row) : 1.f;
+    const auto [m_mean, m_rstd, n_mean, n_rstd] = ahead;
+    const size_t b = size_t(st.gate);
+    const bool gate_ends = st.next(kRows);
+    if (st.valid()) load_stats(row_at(st));
     (void)wait(&full[i], (it / S::kStages) & 1);
 
     float2 dr[kNormGroups][2], n[kNormGroups][2];  // the gradient; the normalised row
@@ -782,6 +787,15 @@ __global__ void __launch_bounds__(kNormBwdThreads, 1)
 #pragma unroll
       for (int j = 0; j < kNormGroups; ++j)
         if (!skip(j)) staged4<TS, TPR, VEC, FULL>(g_r, t, j, a.C, dr[j]);
+    }
+    // the stage of the step before, which every warp has read or is about to have, takes
+    // the step that is a ring ahead of it
+    if (it > 0 && next.valid()) {
+      if (warp == int(it % (kNormThreads / 32)) &&
+          wait(&empty[(it - 1) % S::kStages], ((it - 1) / S::kStages) & 1))
+        copy_step(next, it - 1 + S::kStages);
+      next.next(kRows);
+      __syncwarp();
     }
     if (a.grad_x && live) {
       TS* o = static_cast<TS*>(a.grad_x) + off;
@@ -843,8 +857,7 @@ __global__ void __launch_bounds__(kNormBwdThreads, 1)
       if (lane == 0) mbar_arrive(&empty[i]);
     }
     ++it;
-    const size_t b = size_t(st.gate);
-    if (st.next(kRows)) {
+    if (gate_ends) {
       if (a.s_part) {
         float* o = a.s_part + (size_t(blockIdx.x) + b) * 2 * a.C;
         flush_sums<TPR, VEC>(s1, s_buf, o, a.C);
@@ -853,6 +866,12 @@ __global__ void __launch_bounds__(kNormBwdThreads, 1)
       if (st.valid() && a.gate) set_weight(st.gate);
     }
   }
+  norm_sync();
+  if (*abort_flag && threadIdx.x == 0)  // the last copies may still be landing
+    for (uint32_t j = *copied > uint32_t(S::kStages) ? *copied - S::kStages : 0; j < *copied; ++j)
+      if (!(a.inject_stall && j == 0))
+        (void)mbar_wait_bounded(&full[j % S::kStages], (j / S::kStages) & 1);
+  __syncwarp();
   if (a.t_part) {
     float* o = a.t_part + size_t(blockIdx.x) * 2 * a.C;
     flush_sums<TPR, VEC>(t1, s_buf, o, a.C);
