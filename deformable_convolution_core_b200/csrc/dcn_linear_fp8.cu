@@ -118,6 +118,12 @@ LinearPlan linear_plan(int M, int K, int N, bool row_scales, int sms) {
   p.rows = !row_scales && M <= kRowsKernelMax;
   p.m_tiles = blocks_of(M);
   p.part_pitch = int((int64_t(N) + 3) / 4 * 4);
+  if (p.rows) {  // no tiles, no splits
+    p.bn = p.n_tiles = 0;
+    p.splits = 1;
+    p.kb_per = p.k_blocks;
+    return p;
+  }
   double best = 0;
   for (const TileCost& c : kTileCosts) {
     if (c.bn > 128 && N <= 128) continue;
