@@ -24,8 +24,8 @@
 // What bounds it: a K block's round takes about 1100 cycles, in which its MMAs, its
 // scaled additions and the two handshakes between them overlap only in part.  Each part
 // alone: MMAs and handshakes 690, loads and additions 730.  9216 x 1280 x 5120 takes
-// 73 us (1.65 PFLOP/s) in a short run and 84 under the power cap, 589,824 x 160 x 640,
-// whose bytes need 130, 186 and 219.  Weight gradients, whose columns have a scale each,
+// 75 us (1.6 PFLOP/s) in a short run and 88 under the power cap, 589,824 x 160 x 640,
+// whose bytes need 130, 190 and 230.  Weight gradients, whose columns have a scale each,
 // need a second packed multiply: 1570 cycles a block.
 // Every mbarrier wait is bounded; on expiry the kernel sets the error word, stops
 // issuing work, waits (bounded) for what is in flight, frees its tensor memory and
